@@ -26,6 +26,10 @@ STATUS_SEQLEN_RANGE = 2
 STATUS_WAIT_TIMEOUT = 4
 STATUS_INTERNAL = 8
 STATUS_PAGE_RANGE = 16
+STATUS_GROUP_RANGE = 32
+STATUS_PAGE_REFS = 64
+STATUS_POOL_FULL = 128
+STATUS_INDEX_RANGE = 256
 
 # C-ABI symbols declared in include/gqa.h
 EXPORTED = ("gqa_kv_append", "gqa_decode_workspace_size", "gqa_decode", "gqa_status_string",
@@ -33,7 +37,9 @@ EXPORTED = ("gqa_kv_append", "gqa_decode_workspace_size", "gqa_decode", "gqa_sta
             "gqa_decode_window", "gqa_kv_append_paged", "gqa_decode_paged",
             "gqa_kv_append_multi", "gqa_decode_multi_workspace_size", "gqa_decode_multi",
             "gqa_kv_append_fp8", "gqa_kv_append_paged_fp8", "gqa_decode_fp8",
-            "gqa_decode_paged_fp8", "gqa_kv_append_decode")
+            "gqa_decode_paged_fp8", "gqa_kv_append_decode",
+            "gqa_decode_shared_workspace_size", "gqa_decode_shared", "gqa_decode_shared_paged",
+            "gqa_cross_attend_workspace_size", "gqa_cross_attend")
 
 
 class GQAError(RuntimeError):
@@ -103,6 +109,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                          c_int, c_int, c_int, c_int, ctypes.c_float, vp, vp,
                                          ctypes.c_size_t, i32p, vp]
     lib.gqa_decode_paged_fp8.restype = c_int
+    c_float = ctypes.c_float
+    lib.gqa_decode_shared_workspace_size.argtypes = [c_int] * 7
+    lib.gqa_decode_shared_workspace_size.restype = c_size
+    lib.gqa_decode_shared.argtypes = [vp, vp, vp, i32p, i32p, c_int, c_int, vp, vp, i32p, c_int, c_int,
+                                      c_int, c_int, c_int, c_int, c_float, c_int, vp, vp, c_size,
+                                      i32p, vp]
+    lib.gqa_decode_shared.restype = c_int
+    lib.gqa_decode_shared_paged.argtypes = [vp, vp, vp, i32p, c_int, i32p, i32p, i32p, c_int, c_int,
+                                            c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+                                            c_int, vp, vp, c_size, i32p, vp]
+    lib.gqa_decode_shared_paged.restype = c_int
+    lib.gqa_cross_attend_workspace_size.argtypes = [c_int] * 6
+    lib.gqa_cross_attend_workspace_size.restype = c_size
+    lib.gqa_cross_attend.argtypes = [vp, vp, vp, i32p, i32p, c_int, c_int, c_int, c_int, c_int, c_int,
+                                     c_float, c_int, vp, vp, c_size, i32p, vp]
+    lib.gqa_cross_attend.restype = c_int
     lib.gqa_status_string.argtypes = [c_int]
     lib.gqa_status_string.restype = ctypes.c_char_p
     lib.gqa_set_wait_timeout_ns.argtypes = [ctypes.c_ulonglong]
@@ -383,4 +405,146 @@ def decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
         _ptr(block_table), max_pages, _ptr(seq_lens), B, H_q, H_kv, d, page_size, n_pages,
         float(scale), _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status),
         _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ rows that sequences share
+def _on(stream, first: torch.Tensor, *tensors):
+    """The stream of a call on ``first``'s device.  Every tensor has to be on that device.  A
+    tensor the binding allocates for the call (on the device's current stream) and the call then
+    uses on another stream is kept from reuse until that stream is done with it (_made)."""
+    for t in tensors:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if not first.is_cuda:
+        raise ValueError("libgqa needs CUDA tensors")
+    return torch.cuda.current_stream(first.device) if stream is None else stream
+
+
+def _made(t: torch.Tensor, stream) -> torch.Tensor:
+    if stream != torch.cuda.current_stream(t.device):
+        stream.wait_stream(torch.cuda.current_stream(t.device))  # earlier users of the memory
+        t.record_stream(stream)
+    return t
+
+
+class _Device:
+    """The CUDA device that the library works on is the current one: make it the tensors'."""
+
+    def __init__(self, t: torch.Tensor):
+        self.want = t.device.index
+        self.had = torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.had != self.want:
+            torch.cuda.set_device(self.want)
+
+    def __exit__(self, *exc):
+        if self.had != self.want:
+            torch.cuda.set_device(self.had)
+
+
+def _i32(t: torch.Tensor, shape, name: str) -> torch.Tensor:
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be int32 {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return t
+
+
+def _same(t: torch.Tensor, shape, dtype, name: str) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return t
+
+
+def _out_and_workspace(q, out, workspace, n: int, stream):
+    if n == 0:
+        raise GQAError(-9, "no usable sm_100 device is current, or invalid sizes")
+    if out is None:
+        out = _made(torch.empty(q.shape, dtype=torch.float32, device=q.device), stream)
+    _same(out, q.shape, torch.float32, "out")
+    if workspace is None:
+        workspace = _made(torch.empty(n, dtype=torch.uint8, device=q.device), stream)
+    return out, workspace
+
+
+def shared_workspace_size(B: int, Q: int, P: int, H_q: int, H_kv: int, d: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace decode_shared and decode_shared_paged need on the current device."""
+    return int(load_library().gqa_decode_shared_workspace_size(B, Q, P, H_q, H_kv, d, _DTYPES[dtype]))
+
+
+def decode_shared(q, k_prefix, v_prefix, prefix_lens, group_start, k_cache, v_cache, seq_lens,
+                  scale: float, out=None, workspace=None, status=None, stream=None) -> torch.Tensor:
+    """gqa_decode_shared: the sequences [group_start[g], group_start[g+1]) attend the prefix_lens[g]
+    rows of k_prefix[g], read once for all of them, and then their own seq_lens[b] rows.  q is
+    [B, H_q, d], or [B, Q, H_q, d] for Q query tokens per sequence; returns out of q's shape,
+    float32."""
+    q4 = q if q.dim() == 4 else q.unsqueeze(1)
+    B, Q, H_q, d = q4.shape
+    P, L_prefix, H_kv, _ = k_prefix.shape
+    L_max = k_cache.shape[1]
+    dtype = _dtype(q)
+    for t, n, shape in ((k_prefix, "k_prefix", (P, L_prefix, H_kv, d)), (v_prefix, "v_prefix", (P, L_prefix, H_kv, d)),
+                        (k_cache, "k_cache", (B, L_max, H_kv, d)), (v_cache, "v_cache", (B, L_max, H_kv, d))):
+        _same(t, shape, q.dtype, n)
+    _i32(prefix_lens, (P,), "prefix_lens"), _i32(group_start, (P + 1,), "group_start"), _i32(seq_lens, (B,), "seq_lens")
+    stream = _on(stream, q, k_prefix, v_prefix, prefix_lens, group_start, k_cache, v_cache, seq_lens, out, workspace, status)
+    with _Device(q):
+        out, workspace = _out_and_workspace(q, out, workspace, shared_workspace_size(B, Q, P, H_q, H_kv, d, q.dtype), stream)
+        _check(load_library().gqa_decode_shared(
+            _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_lens), _ptr(group_start), P, L_prefix,
+            _ptr(k_cache), _ptr(v_cache), _ptr(seq_lens), B, Q, H_q, H_kv, d, L_max, float(scale),
+            dtype, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+    return out
+
+
+def decode_shared_paged(q, k_pool, v_pool, block_table, seq_lens, group_start, shared_rows,
+                        scale: float, out=None, workspace=None, status=None, stream=None) -> torch.Tensor:
+    """gqa_decode_shared_paged: decode_paged for sequences [group_start[g], group_start[g+1]) whose
+    first shared_rows[g] rows lie in the same pages, which are read once for all of them.  q is
+    [B, H_q, d] or [B, Q, H_q, d]; returns out of q's shape, float32."""
+    q4 = q if q.dim() == 4 else q.unsqueeze(1)
+    B, Q, H_q, d = q4.shape
+    n_pages, page_size, H_kv, _ = k_pool.shape
+    max_pages = block_table.shape[1]
+    P = shared_rows.shape[0]
+    dtype = _dtype(q)
+    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        _same(t, (n_pages, page_size, H_kv, d), q.dtype, n)
+    _i32(block_table, (B, max_pages), "block_table"), _i32(seq_lens, (B,), "seq_lens")
+    _i32(group_start, (P + 1,), "group_start"), _i32(shared_rows, (P,), "shared_rows")
+    stream = _on(stream, q, k_pool, v_pool, block_table, seq_lens, group_start, shared_rows, out, workspace, status)
+    with _Device(q):
+        out, workspace = _out_and_workspace(q, out, workspace, shared_workspace_size(B, Q, P, H_q, H_kv, d, q.dtype), stream)
+        _check(load_library().gqa_decode_shared_paged(
+            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), max_pages, _ptr(seq_lens),
+            _ptr(group_start), _ptr(shared_rows), P, B, Q, H_q, H_kv, d, page_size, n_pages,
+            float(scale), dtype, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status),
+            _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ cross attention
+def cross_workspace_size(E: int, N: int, H_q: int, H_kv: int, d: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace cross_attend needs on the current device."""
+    return int(load_library().gqa_cross_attend_workspace_size(E, N, H_q, H_kv, d, _DTYPES[dtype]))
+
+
+def cross_attend(q, k_enc, v_enc, enc_lens, q_start, scale: float, out=None, workspace=None,
+                 status=None, stream=None) -> torch.Tensor:
+    """gqa_cross_attend: tokens [q_start[e], q_start[e+1]) of q [N, H_q, d] attend the states
+    [0, enc_lens[e]) of k_enc, v_enc [E, S_max, H_kv, d].  Returns out [N, H_q, d] float32; tokens
+    before q_start[0] or from q_start[E] on are left as they were in ``out``."""
+    N, H_q, d = q.shape
+    E, S_max, H_kv, _ = k_enc.shape
+    dtype = _dtype(q)
+    for t, n in ((k_enc, "k_enc"), (v_enc, "v_enc")):
+        _same(t, (E, S_max, H_kv, d), q.dtype, n)
+    _i32(enc_lens, (E,), "enc_lens"), _i32(q_start, (E + 1,), "q_start")
+    stream = _on(stream, q, k_enc, v_enc, enc_lens, q_start, out, workspace, status)
+    with _Device(q):
+        out, workspace = _out_and_workspace(q, out, workspace, cross_workspace_size(E, N, H_q, H_kv, d, q.dtype), stream)
+        _check(load_library().gqa_cross_attend(
+            _ptr(q), _ptr(k_enc), _ptr(v_enc), _ptr(enc_lens), _ptr(q_start), E, N, H_q, H_kv, d,
+            S_max, float(scale), dtype, _ptr(out), _ptr(workspace), workspace.numel(),
+            _ptr(status), _stream(stream)))
     return out

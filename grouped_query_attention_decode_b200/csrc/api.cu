@@ -12,6 +12,7 @@
 #include "gqa.h"
 #include "launch.h"
 #include "schedule.cuh"
+#include "spans.cuh"
 
 namespace gqa {
 namespace {
@@ -150,11 +151,11 @@ bool encode_cache_map8(CUtensorMap *m, const void *base, int outer, int H_kv, in
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// q as (d, H_q, B*Q); one unit's tile is the box (64 columns, rb heads, Q tokens), which lands
+// q as (d, H_q, tokens); one unit's tile is the box (64 columns, rb heads, Q tokens), which lands
 // in shared memory as rows j * rb + h'.
-bool encode_q_map(CUtensorMap *m, const void *q, int B, int Q, int H_q, int d, int rb) {
+bool encode_q_map(CUtensorMap *m, const void *q, int tokens, int Q, int H_q, int d, int rb) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H_q),
-                                static_cast<cuuint64_t>(B) * Q};
+                                static_cast<cuuint64_t>(tokens)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
                                    static_cast<cuuint64_t>(H_q) * d * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rb), static_cast<cuuint32_t>(Q)};
@@ -343,7 +344,7 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
         const int outer_dim = pg.block_table ? pg.n_pages : B;
         const int box = pg.block_table ? (pg.page_size < p.T ? pg.page_size : p.T) : p.T;
         (void)rp;
-        if (!encode_q_map(&maps.q, q, B, Q, H_q, d, g.rb) ||
+        if (!encode_q_map(&maps.q, q, B * Q, Q, H_q, d, g.rb) ||
             !encode_cache_map(&maps.k, k_cache, outer_dim, H_kv, d, rows_dim, box) ||
             !encode_cache_map(&maps.k8, k_cache, outer_dim, H_kv, d, rows_dim, 8) ||
             !encode_cache_map(&maps.v, v_cache, outer_dim, H_kv, d, rows_dim, box) ||
@@ -558,6 +559,268 @@ extern "C" int gqa_decode_paged_fp8(const void *q, const void *k_pool, const voi
     return decode_impl(q, k_pool, v_pool, seq_lens, B, H_q, H_kv, d, max_pages * page_size, 0,
                        scale, GQA_DTYPE_E4M3, out, workspace, workspace_bytes, status, stream,
                        pg, 1, k_scale, v_scale);
+}
+
+namespace {
+
+// What the span calls share: sizes that follow from the arguments, and the workspace's sections
+// (byte offsets).
+struct SpanPlan {
+    int r, rb, HB, tb, blk, nblkQ, T, RT, unit_rows;
+    long long u1, units, slot_floats;
+    size_t uinfo, slots, res, res_ml, bytes;
+};
+
+// P shared spans over N tokens, and own spans of B sequences (none: B = 0) of Q tokens.
+bool span_plan(SpanPlan &s, int P, int N, int B, int Q, int H_q, int H_kv, int d, gqa_dtype_t dtype, int sms) {
+    const bool tc = dtype == GQA_DTYPE_BF16;
+    s.T = s.RT = tc ? 128 : 64;
+    s.r = H_q / H_kv;
+    s.rb = s.r < s.RT ? s.r : s.RT;
+    s.HB = (s.r + s.rb - 1) / s.rb;
+    s.tb = s.RT / s.rb;
+    // two row tiles per unit on the tensor cores: both use a cached tile while it is in shared memory
+    s.blk = tc ? 2 * s.tb : s.tb;
+    s.unit_rows = tc ? 2 * s.RT : s.RT;
+    s.nblkQ = (Q + s.blk - 1) / s.blk;
+    const long long heads = static_cast<long long>(H_kv) * s.HB;
+    s.u1 = (static_cast<long long>(N) / s.blk + P + 1) * heads;
+    s.units = s.u1 + static_cast<long long>(B) * s.nblkQ * heads;
+    if (heads > 65535 || s.units > (1ll << 30) || static_cast<long long>(N) * H_q > (1ll << 30)) return false;
+    s.slot_floats = static_cast<long long>(s.unit_rows) * (d + 2);
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    s.uinfo = up(static_cast<size_t>(sms) * sizeof(SpanRecord));
+    s.slots = s.uinfo + up(B > 0 ? s.units * sizeof(int4) : 0);
+    s.res = s.slots + up(2ull * sms * s.slot_floats * 4);
+    const size_t rows = B > 0 ? 2ull * N * H_q : 0;
+    s.res_ml = s.res + up(rows * d * 4);
+    s.bytes = s.res_ml + up(rows * 8);
+    return true;
+}
+
+size_t span_workspace(int P, long long N, int B, int Q, int H_q, int H_kv, int d, gqa_dtype_t dtype) {
+    if (P < 1 || N < 1 || N > (1ll << 30) || check_shape(1, H_q, H_kv, d, 1, dtype) != GQA_OK) return 0;
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
+    SpanPlan s;
+    return sms > 0 && span_plan(s, P, static_cast<int>(N), B, Q, H_q, H_kv, d, dtype, sms) ? s.bytes : 0;
+}
+
+// The arrays and sizes of one span call; own caches are absent for cross attention.
+struct SpanArgs {
+    const void *q = nullptr, *k_shared = nullptr, *v_shared = nullptr, *k_own = nullptr, *v_own = nullptr;
+    const int32_t *gstart = nullptr, *glen = nullptr, *lens = nullptr, *block_table = nullptr;
+    int P = 0, N = 0, B = 0, Q = 1, H_q = 0, H_kv = 0, d = 0, g_max = 0, own_max = 0;
+    int max_pages = 0, page_size = 0, n_pages = 0;
+};
+
+int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, void *workspace, size_t workspace_bytes,
+              int32_t *status, cudaStream_t stream) {
+    const int rc = check_shape(1, a.H_q, a.H_kv, a.d, a.g_max, dtype);
+    if (rc != GQA_OK) return rc;
+    if (a.P <= 0 || a.N <= 0 || (a.B > 0 && a.own_max <= 0)) return GQA_ERR_SHAPE;
+    if (!workspace) return GQA_ERR_WORKSPACE;
+    for (const void *p : {a.q, a.k_shared, a.v_shared, a.k_own, a.v_own, static_cast<const void *>(out)})
+        if (!aligned(p, 16)) return GQA_ERR_ALIGNMENT;
+    for (const int32_t *p : {a.gstart, a.glen, a.lens, a.block_table, static_cast<const int32_t *>(status)})
+        if (!aligned(p, 4)) return GQA_ERR_ALIGNMENT;
+    if (!aligned(workspace, 256)) return GQA_ERR_ALIGNMENT;
+    if (!std::isfinite(scale)) return GQA_ERR_SHAPE;
+    int dev = 0;
+    const int sms = current_sm_count(&dev);
+    if (sms <= 0) return GQA_ERR_NO_DEVICE;
+    SpanPlan s;
+    if (!span_plan(s, a.P, a.N, a.B, a.Q, a.H_q, a.H_kv, a.d, dtype, sms)) return GQA_ERR_SHAPE;
+    if (workspace_bytes < s.bytes) return GQA_ERR_WORKSPACE;
+
+    const bool paged = a.block_table != nullptr, tc = dtype == GQA_DTYPE_BF16;
+    SpanParams p = {};
+    p.gstart = a.gstart;
+    p.glen = a.glen;
+    p.P = a.P;
+    p.g_max = a.g_max;
+    p.g_step = paged ? a.page_size : 1;
+    p.lens = a.lens;
+    p.B = a.B;
+    p.own_max = a.own_max;
+    p.own_after = paged;
+    p.Q = a.Q;
+    p.N = a.N;
+    p.H_q = a.H_q;
+    p.H_kv = a.H_kv;
+    p.d = a.d;
+    p.r = s.r;
+    p.rb = s.rb;
+    p.HB = s.HB;
+    p.tb = s.tb;
+    p.blk = s.blk;
+    p.nblkQ = s.nblkQ;
+    p.T = s.T;
+    p.RT = s.RT;
+    p.unit_rows = s.unit_rows;
+    p.u1 = static_cast<int>(s.u1);
+    p.block_table = a.block_table;
+    p.max_pages = a.max_pages;
+    p.page_size = a.page_size;
+    p.n_pages = a.n_pages;
+    p.wait_ns = g_wait_ns.load();
+    p.out = out;
+    p.status = status;
+    // One CTA per SM, but no more than there can be tiles.
+    const long long tiles_g = (static_cast<long long>(a.g_max) + s.T - 1) / s.T, tiles_o = (static_cast<long long>(a.own_max) + s.T - 1) / s.T;
+    const long long most = s.u1 * tiles_g + (s.units - s.u1) * tiles_o;
+    p.G = most < sms ? static_cast<int>(most) : sms;
+    const double scale_log2 = static_cast<double>(scale) * 1.4426950408889634;
+    p.scale_log2 = static_cast<float>(scale_log2);
+    if (tc) {
+        // The bf16 kernel finds a row's maximum before it scales, so the sign goes to q; and it
+        // masks by -infinity, which times 0 would be NaN: a scale whose products all round to 0
+        // stands in for 0.
+        p.negate = scale_log2 < 0;
+        p.scale_log2 = static_cast<float>(std::fabs(scale_log2));
+        if (p.scale_log2 < 1e-37f) p.scale_log2 = 1e-37f;
+    }
+    auto *w = static_cast<unsigned char *>(workspace);
+    p.rec = reinterpret_cast<SpanRecord *>(w);
+    p.uinfo = reinterpret_cast<int4 *>(w + s.uinfo);
+    p.slots = reinterpret_cast<float *>(w + s.slots);
+    p.slot_floats = s.slot_floats;
+    p.res = reinterpret_cast<float *>(w + s.res);
+    p.res_ml = reinterpret_cast<float *>(w + s.res_ml);
+
+    int res;
+    if (tc) {
+        if (encode_fn() == nullptr) return GQA_ERR_CUDA;
+        SpanMaps m;
+        // caches as (d, H_kv, rows, prefixes or sequences) or (d, H_kv, page_size, n_pages)
+        const int box = paged && a.page_size < s.T ? a.page_size : s.T;
+        const int rows_g = paged ? a.page_size : a.g_max, rows_o = paged ? a.page_size : a.own_max;
+        const int outer_g = paged ? a.n_pages : a.P, outer_o = paged ? a.n_pages : a.B;
+        if (!encode_q_map(&m.q_shared, a.q, a.N, s.tb, a.H_q, a.d, s.rb) ||
+            !encode_cache_map(&m.k_shared, a.k_shared, outer_g, a.H_kv, a.d, rows_g, box) ||
+            !encode_cache_map(&m.k_shared8, a.k_shared, outer_g, a.H_kv, a.d, rows_g, 8) ||
+            !encode_cache_map(&m.v_shared, a.v_shared, outer_g, a.H_kv, a.d, rows_g, box) ||
+            !encode_cache_map(&m.v_shared8, a.v_shared, outer_g, a.H_kv, a.d, rows_g, 8))
+            return GQA_ERR_SHAPE;
+        m.q_own = m.q_shared;
+        m.k_own = m.k_shared;
+        m.k_own8 = m.k_shared8;
+        m.v_own = m.v_shared;
+        m.v_own8 = m.v_shared8;
+        if (a.B > 0 && !encode_q_map(&m.q_own, a.q, a.N, a.Q < s.tb ? a.Q : s.tb, a.H_q, a.d, s.rb)) return GQA_ERR_SHAPE;
+        if (a.B > 0 && !paged &&
+            (!encode_cache_map(&m.k_own, a.k_own, outer_o, a.H_kv, a.d, rows_o, box) ||
+             !encode_cache_map(&m.k_own8, a.k_own, outer_o, a.H_kv, a.d, rows_o, 8) ||
+             !encode_cache_map(&m.v_own, a.v_own, outer_o, a.H_kv, a.d, rows_o, box) ||
+             !encode_cache_map(&m.v_own8, a.v_own, outer_o, a.H_kv, a.d, rows_o, 8)))
+            return GQA_ERR_SHAPE;
+        res = launch_span_tc(m, p, stream);
+    } else {
+        res = launch_span_f32(p, static_cast<const float *>(a.q), static_cast<const float *>(a.k_shared),
+                              static_cast<const float *>(a.v_shared), static_cast<const float *>(a.k_own),
+                              static_cast<const float *>(a.v_own), stream);
+    }
+    return res != GQA_OK ? res : launch_span_merge(p, stream);
+}
+
+}  // namespace
+
+extern "C" size_t gqa_decode_shared_workspace_size(int B, int Q, int P, int H_q, int H_kv, int d, gqa_dtype_t dtype) {
+    if (B < 1 || Q < 1 || Q > kMaxUnitCols) return 0;
+    return span_workspace(P, static_cast<long long>(B) * Q, B, Q, H_q, H_kv, d, dtype);
+}
+
+extern "C" size_t gqa_cross_attend_workspace_size(int E, int N, int H_q, int H_kv, int d, gqa_dtype_t dtype) {
+    return span_workspace(E, N, 0, 1, H_q, H_kv, d, dtype);
+}
+
+extern "C" int gqa_decode_shared(const void *q, const void *k_prefix, const void *v_prefix,
+                                 const int32_t *prefix_lens, const int32_t *group_start, int P,
+                                 int L_prefix, const void *k_cache, const void *v_cache,
+                                 const int32_t *seq_lens, int B, int Q, int H_q, int H_kv, int d,
+                                 int L_max, float scale, gqa_dtype_t dtype, float *out,
+                                 void *workspace, size_t workspace_bytes, int32_t *status,
+                                 cudaStream_t stream) {
+    if (!q || !k_prefix || !v_prefix || !prefix_lens || !group_start || !k_cache || !v_cache || !seq_lens || !out)
+        return GQA_ERR_NULL;
+    if (B <= 0 || Q < 1 || Q > kMaxUnitCols || static_cast<long long>(B) * Q > (1ll << 30)) return GQA_ERR_SHAPE;
+    SpanArgs a;
+    a.q = q;
+    a.k_shared = k_prefix;
+    a.v_shared = v_prefix;
+    a.k_own = k_cache;
+    a.v_own = v_cache;
+    a.gstart = group_start;
+    a.glen = prefix_lens;
+    a.lens = seq_lens;
+    a.P = P;
+    a.N = B * Q;
+    a.B = B;
+    a.Q = Q;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.d = d;
+    a.g_max = L_prefix;
+    a.own_max = L_max;
+    return span_impl(a, scale, dtype, out, workspace, workspace_bytes, status, stream);
+}
+
+extern "C" int gqa_decode_shared_paged(const void *q, const void *k_pool, const void *v_pool,
+                                       const int32_t *block_table, int max_pages,
+                                       const int32_t *seq_lens, const int32_t *group_start,
+                                       const int32_t *shared_rows, int P, int B, int Q, int H_q,
+                                       int H_kv, int d, int page_size, int n_pages, float scale,
+                                       gqa_dtype_t dtype, float *out, void *workspace,
+                                       size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
+    if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !group_start || !shared_rows || !out)
+        return GQA_ERR_NULL;
+    if (B <= 0 || Q < 1 || Q > kMaxUnitCols || static_cast<long long>(B) * Q > (1ll << 30)) return GQA_ERR_SHAPE;
+    if (max_pages <= 0 || n_pages <= 0 || page_size <= 0 || page_size % 8 != 0 ||
+        static_cast<long long>(max_pages) * page_size > (1ll << 30))
+        return GQA_ERR_SHAPE;
+    // a tile of 128 rows must lie in one page or cover whole pages
+    if (dtype == GQA_DTYPE_BF16 && 128 % page_size != 0 && page_size % 128 != 0) return GQA_ERR_SHAPE;
+    SpanArgs a;
+    a.q = q;
+    a.k_shared = a.k_own = k_pool;
+    a.v_shared = a.v_own = v_pool;
+    a.gstart = group_start;
+    a.glen = shared_rows;
+    a.lens = seq_lens;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.n_pages = n_pages;
+    a.P = P;
+    a.N = B * Q;
+    a.B = B;
+    a.Q = Q;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.d = d;
+    a.g_max = a.own_max = max_pages * page_size;
+    return span_impl(a, scale, dtype, out, workspace, workspace_bytes, status, stream);
+}
+
+extern "C" int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc,
+                                const int32_t *enc_lens, const int32_t *q_start, int E, int N,
+                                int H_q, int H_kv, int d, int S_max, float scale,
+                                gqa_dtype_t dtype, float *out, void *workspace,
+                                size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
+    if (!q || !k_enc || !v_enc || !enc_lens || !q_start || !out) return GQA_ERR_NULL;
+    SpanArgs a;
+    a.q = q;
+    a.k_shared = k_enc;
+    a.v_shared = v_enc;
+    a.gstart = q_start;
+    a.glen = enc_lens;
+    a.P = E;
+    a.N = N;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.d = d;
+    a.g_max = S_max;
+    return span_impl(a, scale, dtype, out, workspace, workspace_bytes, status, stream);
 }
 
 extern "C" const char *gqa_status_string(int code) {

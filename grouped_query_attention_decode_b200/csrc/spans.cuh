@@ -1,0 +1,298 @@
+// Work partition of the span kernels: groups of query rows, each group against one span of
+// cached rows.
+//
+// A span is either a shared one -- the tokens of a group of sequences (or of one encoder
+// sequence) against the rows they all attend -- or one sequence's own rows.  Per key/value head
+// a span's query rows are (token, query head of the group) pairs; they are cut into units of up
+// to `blk` tokens and rb heads, and a unit's cached rows into tiles of T.  As in schedule.cuh
+// the tiles of all units form one line, CTA i of G takes the tiles
+//     [floor(i * total / G), floor((i + 1) * total / G)),
+// and every CTA derives its range from the lengths on the device.  A unit that lies in one CTA's
+// range is whole; the pieces of the others go to workspace slots (two per CTA: only a range's
+// first and last piece can be partial) and are joined by the kernel launched behind
+// (span_merge.cu):  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the pieces c.
+#pragma once
+
+#include <cstdint>
+
+#include "device.cuh"
+#include "gqa.h"
+#include "schedule.cuh"
+
+namespace gqa {
+
+struct SpanParams {
+    // shared spans: group g holds the members [gstart[g], gstart[g + 1]) and attends glen[g] rows
+    const int32_t *gstart, *glen;
+    int P, g_max;
+    int g_step;  // glen has to be a multiple of this (the page size; 1 for contiguous caches)
+    // own spans, none when B = 0: sequence b attends lens[b] rows of its own cache, or, with
+    // own_after (paged), the rows [glen[its group], lens[b]) of its block table
+    const int32_t *lens;
+    int B, own_max, own_after;
+    int Q, N;  // tokens per member (1 for cross attention), tokens in all
+    int H_q, H_kv, d, r;
+    int rb, HB, tb;  // heads per row tile, head blocks = ceil(r / rb), tokens per row tile
+    int blk;         // tokens per unit: one or two row tiles
+    int nblkQ;       // units of one own span and head block: ceil(Q / blk)
+    int T, RT;       // cached rows per tile, query rows per row tile
+    int G;
+    const int32_t *block_table;  // nullptr: contiguous caches
+    int max_pages, page_size, n_pages;
+    float scale_log2;  // softmax scale * log2(e); the bf16 kernel takes its magnitude ...
+    int negate;        // ... and the sign here
+    unsigned long long wait_ns;
+    float *out;
+    int32_t *status;
+    // workspace
+    int4 *uinfo;           // own spans present: [unit] (first CTA, its slot, last CTA, 0)
+    struct SpanRecord *rec;  // no own spans: [CTA] the cut unit that starts there; else [0].total
+    float *slots;          // [2 * G][slot_floats]
+    long long slot_floats;
+    float *res, *res_ml;   // [2][N * H_q][d] sums and [2][N * H_q][2] (m, l) of whole units
+    int u1;                // first unit number of the own spans
+    int unit_rows;         // query rows of a slot
+};
+
+struct SpanRecord {
+    long long total;
+    int valid, tok0, ntok, kvh, hb, k0, c1, pad;
+};
+
+// The group that member i belongs to, -1 for none: the last g with gstart[g] <= i.
+__device__ __forceinline__ int group_of(const SpanParams &p, int i) {
+    int lo = 0, hi = p.P + 1;  // first index whose start is past i lies in [lo, hi]
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.gstart + mid) > i) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo - 1 < p.P ? lo - 1 : -1;
+}
+
+// Rows group g shares, or -1 when the entry is out of range.
+__device__ __forceinline__ int shared_rows_of(const SpanParams &p, int g) {
+    const int n = __ldg(p.glen + g);
+    return n < 0 || n > p.g_max || n % p.g_step != 0 ? -1 : n;
+}
+
+// First own row and number of own rows of sequence b; false when its length (or its group's) is
+// out of range.
+__device__ __forceinline__ bool own_rows_of(const SpanParams &p, int b, int &row0, int &rows) {
+    const int n = __ldg(p.lens + b);
+    row0 = rows = 0;
+    if (p.own_after) {
+        const int g = group_of(p, b);
+        if (g >= 0) row0 = shared_rows_of(p, g);
+        if (row0 < 0) return row0 = 0, false;
+    }
+    if (n < row0 || n > p.own_max || (p.Q > 1 && n - row0 < p.Q)) return false;
+    rows = n - row0;
+    return true;
+}
+
+struct Span {
+    int tok0, ntok;  // its tokens
+    int row0, rows;  // its cached rows within the source
+    int src;         // contiguous: prefix / encoder sequence / sequence; paged: block-table row
+};
+
+__device__ inline Span span_at(const SpanParams &p, int s, bool flag) {
+    Span sp = {0, 0, 0, 0, 0};
+    int bad = 0;
+    if (s < p.P) {
+        const int a = __ldg(p.gstart + s), e = __ldg(p.gstart + s + 1);
+        if (a < 0 || e < a || e > (p.B > 0 ? p.B : p.N)) {
+            bad = GQA_STATUS_GROUP_RANGE;
+        } else {
+            const int n = shared_rows_of(p, s);
+            if (n < 0) bad = GQA_STATUS_SEQLEN_RANGE;
+            sp.tok0 = a * p.Q;
+            sp.ntok = (e - a) * p.Q;
+            sp.rows = max(n, 0);
+            sp.src = p.block_table != nullptr ? a : s;
+        }
+    } else if (s < p.P + p.B) {
+        const int b = s - p.P;
+        if (!own_rows_of(p, b, sp.row0, sp.rows)) bad = GQA_STATUS_SEQLEN_RANGE;
+        sp.tok0 = b * p.Q;
+        sp.ntok = p.Q;
+        sp.src = b;
+    }
+    if (flag && bad != 0 && p.status != nullptr) atomicOr(p.status, bad);
+    return sp;
+}
+
+__device__ __forceinline__ int span_blocks(const SpanParams &p, const Span &sp) { return (sp.ntok + p.blk - 1) / p.blk; }
+
+__device__ __forceinline__ long long span_tiles(const SpanParams &p, const Span &sp) {
+    return static_cast<long long>(tiles_of(sp.rows, p.T)) * span_blocks(p, sp) * p.H_kv * p.HB;
+}
+
+// Unit number of block `block` of span s.  Shared spans: blocks are numbered by their first
+// token / blk + group, which grows along the line, so no two blocks share a number.
+__device__ __forceinline__ int unit_number(const SpanParams &p, int s, int tok0, int block, int kvh, int hb) {
+    const int k = s < p.P ? tok0 / p.blk + block + s : (s - p.P) * p.nblkQ + block;
+    return (s < p.P ? 0 : p.u1) + (k * p.H_kv + kvh) * p.HB + hb;
+}
+
+struct SpanRange {
+    long long begin, end, total, off0;
+    int s0;
+};
+
+// Whole CTA of NT threads: the total number of tiles, this CTA's range and the span it starts
+// in.  `scratch`: NT / 32 long longs of shared memory; `res`: shared.
+template <int NT>
+__device__ void locate_span_range(const SpanParams &p, int cta, long long *scratch, SpanRange *res) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int spans = p.P + p.B, per = (spans + NT - 1) / NT;
+    const int s0 = tid * per, s1 = min(spans, s0 + per);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += span_tiles(p, span_at(p, s, cta == 0));
+    const long long incl = warp_incl_scan(mine, lane);
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long off = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) off += scratch[w];
+        total += scratch[w];
+    }
+    const long long begin = cta_range_begin(cta, total, p.G), end = cta_range_begin(cta + 1, total, p.G);
+    if (tid == 0) {
+        res->begin = begin;
+        res->end = end;
+        res->total = total;
+        if (begin >= end) res->s0 = 0, res->off0 = 0;
+    }
+    if (begin < end && off <= begin && begin < off + mine) {
+        for (int s = s0; s < s1; ++s) {
+            const long long v = span_tiles(p, span_at(p, s, false));
+            if (begin < off + v) {
+                res->s0 = s;
+                res->off0 = off;
+                break;
+            }
+            off += v;
+        }
+    }
+    __syncthreads();
+}
+
+// One CTA-range piece of one unit.
+struct SpanSegment {
+    int s, src;
+    int tok0, ntok;   // tokens of the unit
+    int kvh, hb;
+    int row0, rows;   // cached rows of the span within its source
+    int j0, len, nt;  // first tile and tiles of the piece, tiles of the unit
+    int unit;
+    long long uoff;   // line position of the unit's first tile
+    bool first;       // the piece opens the CTA's range (its slot is 0, else 1)
+    __device__ __forceinline__ bool whole() const { return len == nt; }
+};
+
+struct SpanWalker {
+    long long t, end, off;
+    int s, nt, nblk;
+    Span sp;
+    bool opened;
+
+    __device__ void load(const SpanParams &p) {
+        sp = span_at(p, s, false);
+        nt = tiles_of(sp.rows, p.T);
+        nblk = span_blocks(p, sp);
+    }
+    __device__ void init(const SpanParams &p, const SpanRange &cr) {
+        t = cr.begin;
+        end = cr.end;
+        off = cr.off0;
+        s = cr.s0;
+        opened = false;
+        nt = nblk = 0;
+        if (t < end) load(p);
+    }
+    __device__ bool next(const SpanParams &p, SpanSegment &g) {
+        if (t >= end) return false;
+        const int hv = p.H_kv * p.HB;
+        while (t >= off + static_cast<long long>(nt) * nblk * hv) {
+            off += static_cast<long long>(nt) * nblk * hv;
+            if (++s >= p.P + p.B) {  // cannot happen while t < total
+                t = end;
+                return false;
+            }
+            load(p);
+        }
+        const long long rel = t - off;
+        const int k = static_cast<int>(udiv(rel, nt));
+        const int h = k / nblk, block = k - h * nblk;
+        g.s = s;
+        g.src = sp.src;
+        g.tok0 = sp.tok0 + block * p.blk;
+        g.ntok = min(p.blk, sp.ntok - block * p.blk);
+        g.kvh = h / p.HB;
+        g.hb = h - g.kvh * p.HB;
+        g.row0 = sp.row0;
+        g.rows = sp.rows;
+        g.j0 = static_cast<int>(rel - static_cast<long long>(k) * nt);
+        const long long left = end - t;
+        g.len = static_cast<int>(left < nt - g.j0 ? left : nt - g.j0);
+        g.nt = nt;
+        g.unit = unit_number(p, s, sp.tok0, block, g.kvh, g.hb);
+        g.uoff = off + static_cast<long long>(k) * nt;
+        g.first = !opened;
+        opened = true;
+        t += g.len;
+        return true;
+    }
+};
+
+// Row of q and out that row i of a unit's row tile stands for, -1 for padding.  `token` gets the
+// row's token.
+__device__ __forceinline__ long long span_row(const SpanParams &p, const SpanSegment &g, int tile, int i, int &token) {
+    const int tl = tile * p.tb + i / p.rb, h = g.hb * p.rb + i % p.rb;
+    token = g.tok0 + tl;
+    if (i >= p.tb * p.rb || tl >= g.ntok || h >= p.r) return -1;
+    return static_cast<long long>(token) * p.H_q + g.kvh * p.r + h;
+}
+
+// Own rows that token `token` of its sequence sees: the Q tokens are the last Q of the rows and
+// token j sees one fewer than token j + 1.
+__device__ __forceinline__ int seen_rows(const SpanParams &p, const SpanSegment &g, int token) {
+    return g.s < p.P || p.Q == 1 ? g.rows : g.rows - p.Q + 1 + token % p.Q;
+}
+
+// One thread of a CTA, before its segments.
+__device__ __forceinline__ void open_notes(const SpanParams &p, const SpanRange &cr) {
+    if (p.B == 0) p.rec[blockIdx.x].valid = 0;
+    else if (blockIdx.x == 0) p.rec[0].total = cr.total;
+}
+
+// The same thread, once per segment: what the merge needs to find the unit's pieces.
+__device__ inline void note_unit(const SpanParams &p, const SpanSegment &g, const SpanRange &cr) {
+    if (g.j0 != 0) return;
+    const int c0 = blockIdx.x;
+    const int c1 = g.whole() ? c0 : static_cast<int>(cta_of_tile(g.uoff + g.nt - 1, cr.total, p.G));
+    if (p.B > 0) {
+        p.uinfo[g.unit] = make_int4(c0, g.first ? 0 : 1, c1, 0);
+    } else if (!g.whole()) {
+        p.rec[c0] = SpanRecord{cr.total, 1, g.tok0, g.ntok, g.kvh, g.hb, g.first ? 0 : 1, c1, 0};
+    }
+}
+
+// TMA descriptors of one bf16 call: q in boxes of a shared span's row tile (tb tokens) and of an
+// own span's (min(tb, Q) tokens); K and V of the shared rows and of the own rows, each in boxes
+// of a tile (or a page) and of 8 rows.
+struct SpanMaps {
+    CUtensorMap q_shared, q_own;
+    CUtensorMap k_shared, k_shared8, v_shared, v_shared8;
+    CUtensorMap k_own, k_own8, v_own, v_own8;
+};
+
+int launch_span_tc(const SpanMaps &maps, const SpanParams &p, cudaStream_t stream);
+int launch_span_f32(const SpanParams &p, const float *q, const float *ks, const float *vs, const float *ko,
+                    const float *vo, cudaStream_t stream);
+int launch_span_merge(const SpanParams &p, cudaStream_t stream);
+
+}  // namespace gqa

@@ -82,6 +82,15 @@ typedef enum {
 #define GQA_STATUS_PAGE_RANGE 16      /* paged calls: a block-table entry a row needs is outside
                                          [0, n_pages); page 0 was read instead, the affected
                                          outputs are not valid */
+#define GQA_STATUS_GROUP_RANGE 32     /* gqa_decode_shared*, gqa_cross_attend: a group's start is
+                                         negative, past its end, or past the batch; the group
+                                         shares nothing (its tokens' outputs are not valid) */
+#define GQA_STATUS_PAGE_REFS 64       /* gqa_pages_*: a page's count of holders would fall below
+                                         zero; it is left at zero */
+#define GQA_STATUS_POOL_FULL 128      /* gqa_pages_reserve: not enough free pages; the sequences
+                                         from the first that found none on got nothing */
+#define GQA_STATUS_INDEX_RANGE 256    /* gqa_pages_*: a sequence or page number in an argument is
+                                         out of range; it is skipped */
 
 /*
  * gqa_kv_append: write this step's key and value vectors into the cache.
@@ -282,6 +291,74 @@ int gqa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
                          int max_pages, const int32_t *seq_lens, int B, int H_q, int H_kv, int d,
                          int page_size, int n_pages, float scale, float *out, void *workspace,
                          size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
+/*
+ * Sequences that share rows.  Samples of one prompt, conversations under one system prompt and
+ * the beams of a search attend the same leading rows; these calls read those rows once per group
+ * of sequences instead of once per sequence ("GQA 阅读笔记", Algorithm 2 notes: a cached vector is
+ * read once for all the queries that attend it -- here across sequences as well as heads).
+ *
+ * Group g (0 <= g < P) is the sequences [group_start[g], group_start[g + 1]); group_start [P + 1]
+ * int32 (device) must not decrease and must lie in [0, B] (GQA_STATUS_GROUP_RANGE otherwise).
+ * Sequences outside every group share nothing.  q [B][Q][H_q][d] holds Q query tokens per
+ * sequence, 1 <= Q <= 32, which are the last Q of its own rows, as in gqa_decode_multi.  out
+ * [B][Q][H_q][d] float32.
+ *
+ * gqa_decode_shared: contiguous caches.  The rows that group g shares are k_prefix, v_prefix
+ *   [P][L_prefix][H_kv][d], rows [0, prefix_lens[g]); a sequence attends them and then the
+ *   seq_lens[b] rows of its own cache [B][L_max][H_kv][d] (token j: own rows
+ *   [0, seq_lens[b] - Q + 1 + j)).  Either may be empty; both empty give out[b] = 0.
+ * gqa_decode_shared_paged: the result of gqa_decode_paged (for Q > 1: of gqa_decode_multi) over
+ *   the same pools, block_table [B][max_pages] and seq_lens, for tables in which the sequences of
+ *   group g hold their first shared_rows[g] rows in the same pages (as gqa_pages_fork leaves
+ *   them).  Those rows are read through the table of the group's first sequence.  shared_rows[g]
+ *   must be a multiple of page_size and at most seq_lens[b] (- Q for Q > 1) of every sequence of
+ *   the group.  page_size must be a multiple of 8 and divide 128 or be a multiple of 128 (any
+ *   multiple of 8 for float32).
+ * A length out of range -- negative, past its capacity, own rows < Q (Q > 1), shared rows that do
+ * not fit the rules above -- gives out[b] = 0 for the sequences concerned and sets
+ * GQA_STATUS_SEQLEN_RANGE.  bfloat16 (tensor cores) and float32 (CUDA cores).  P >= 1, d, heads and
+ * alignment as for gqa_decode.  The workspace needs gqa_decode_shared_workspace_size() bytes and
+ * no zero-fill; two calls that may run at the same time must not share one.  Launches two kernels
+ * on `stream`.
+ */
+size_t gqa_decode_shared_workspace_size(int B, int Q, int P, int H_q, int H_kv, int d,
+                                        gqa_dtype_t dtype);
+int gqa_decode_shared(const void *q, const void *k_prefix, const void *v_prefix,
+                      const int32_t *prefix_lens, const int32_t *group_start, int P, int L_prefix,
+                      const void *k_cache, const void *v_cache, const int32_t *seq_lens, int B,
+                      int Q, int H_q, int H_kv, int d, int L_max, float scale, gqa_dtype_t dtype,
+                      float *out, void *workspace, size_t workspace_bytes, int32_t *status,
+                      cudaStream_t stream);
+int gqa_decode_shared_paged(const void *q, const void *k_pool, const void *v_pool,
+                            const int32_t *block_table, int max_pages, const int32_t *seq_lens,
+                            const int32_t *group_start, const int32_t *shared_rows, int P, int B,
+                            int Q, int H_q, int H_kv, int d, int page_size, int n_pages,
+                            float scale, gqa_dtype_t dtype, float *out, void *workspace,
+                            size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
+/*
+ * gqa_cross_attend: attention of decoder tokens over an encoder's states, whose number is
+ * another.  ("从MHA到GQA" gives the attention of one sequence's queries over another's keys; the
+ * T5 models of "GQA 阅读笔记" are encoder-decoder models.)  The N tokens are packed: those of
+ * encoder sequence e are [q_start[e], q_start[e + 1]) -- one token of a decoding step, one per
+ * beam, or a whole target sequence -- and each attends all of the states [0, enc_lens[e]); there
+ * is no mask among tokens.
+ *     out[i][h][:] = sum_t softmax_t( scale * q[i][h] . k_enc[e][t][h/r] ) * v_enc[e][t][h/r][:]
+ *   q        [N][H_q][d];  out [N][H_q][d] float32
+ *   k_enc, v_enc [E][S_max][H_kv][d], rows [0, enc_lens[e]) are read
+ *   enc_lens [E] int32; 0 gives zeros, outside [0, S_max] too, with GQA_STATUS_SEQLEN_RANGE
+ *   q_start  [E + 1] int32, must not decrease and must lie in [0, N] (GQA_STATUS_GROUP_RANGE
+ *            otherwise, and that sequence's tokens are not written).  Tokens before q_start[0] and
+ *            from q_start[E] on are neither read nor written.
+ * Types, d, heads, alignment and errors as gqa_decode; the workspace needs
+ * gqa_cross_attend_workspace_size() bytes and no zero-fill.  Launches two kernels on `stream`.
+ */
+size_t gqa_cross_attend_workspace_size(int E, int N, int H_q, int H_kv, int d, gqa_dtype_t dtype);
+int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const int32_t *enc_lens,
+                     const int32_t *q_start, int E, int N, int H_q, int H_kv, int d, int S_max,
+                     float scale, gqa_dtype_t dtype, float *out, void *workspace,
+                     size_t workspace_bytes, int32_t *status, cudaStream_t stream);
 
 /*
  * gqa_decode_noalloc: gqa_decode without a caller-provided workspace.  (The pages have no

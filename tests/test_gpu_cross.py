@@ -1,0 +1,122 @@
+"""GPU parity of cross attention (gqa_cross_attend) against float64.  States past every length hold
+NaN."""
+import pytest
+import torch
+
+import grouped_query_attention_decode_b200 as gqa
+from span_ref import attend64, normal, tolerance
+
+pytestmark = pytest.mark.gpu
+
+
+def make(tokens, states, heads, dtype, before=0, behind=0, seed=7, S_max=None):
+    H_q, H_kv, d = heads
+    g = torch.Generator().manual_seed(seed)
+    starts = [before + sum(tokens[:i]) for i in range(len(tokens) + 1)]
+    S = S_max or max(1, max(states)) + 3
+    x = {"q": normal((starts[-1] + behind, H_q, d), g, dtype), "starts": starts, "states": states}
+    for n in ("k", "v"):
+        x[n] = normal((len(tokens), S, H_kv, d), g, dtype)
+        for e, m in enumerate(states):
+            x[n][e, max(0, m):] = float("nan")
+    return x
+
+
+def run(x, scale, out=None, **kw):
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = gqa.cross_attend(x["q"].cuda(), x["k"].cuda(), x["v"].cuda(), i32(x["states"]), i32(x["starts"]), scale, out=out,
+                           status=status, **kw)
+    torch.cuda.synchronize()
+    return out, int(status.item())
+
+
+def check(x, out, scale):
+    bound = tolerance(x["q"], [x["k"]], [x["v"]], scale, max(x["states"]))
+    for e, n in enumerate(x["states"]):
+        k, v = x["k"][e, :n].cuda(), x["v"][e, :n].cuda()
+        for i in range(x["starts"][e], x["starts"][e + 1]):
+            ref = attend64(x["q"][i].cuda(), k, v, scale)
+            err = float((out[i].double() - ref).abs().max())
+            assert err <= bound, (e, i, err, bound)  # NaN fails too
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (64, 8, 128), (7, 7, 64), (24, 2, 128), (160, 1, 64), (5, 1, 128)], ids=lambda h: "%d_%d_%d" % h)
+def test_heads(heads, dtype):
+    x = make([1, 4, 70], [200, 129, 333], heads, dtype)
+    scale = heads[2] ** -0.5
+    out, status = run(x, scale)
+    assert status == 0
+    check(x, out, scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", [
+    ([1], [1]),
+    ([1, 1, 1], [0, 127, 128]),
+    ([0, 5, 0], [64, 65, 66]),      # encoder sequences that no token attends
+    ([33, 64, 65], [0, 256, 255]),  # tokens whose encoder sequence has no states
+    ([200], [3000]),                # cut over many CTAs
+    ([3] * 40, list(range(1, 401, 10))),
+], ids=["one", "none", "idle", "empty", "cut", "many"])
+def test_lengths(case, dtype):
+    x = make(*case, (16, 4, 64), dtype)
+    out, status = run(x, 0.125)
+    assert status == 0
+    check(x, out, 0.125)
+
+
+def test_tokens_outside_are_left():
+    x = make([2, 3], [100, 0], (8, 2, 64), torch.bfloat16, before=2, behind=3)
+    out, status = run(x, 0.1, out=torch.full((10, 8, 64), 7.0, device="cuda"))
+    assert status == 0
+    check(x, out, 0.1)
+    assert (out[:2] == 7).all() and (out[7:] == 7).all() and not out[4:7].any()
+
+
+def test_out_of_range_is_reported():
+    x = make([2, 3, 2], [100, 90, 80], (8, 2, 64), torch.bfloat16)
+    good, _ = run(x, 0.1)
+    for bad in (-1, 1000):
+        out, status = run(dict(x, states=[100, bad, 80]), 0.1)
+        assert status == gqa.STATUS_SEQLEN_RANGE
+        assert torch.equal(out[:2], good[:2]) and torch.equal(out[5:], good[5:]) and not out[2:5].any()
+    out, status = run(dict(x, starts=[0, 2, 5, 8]), 0.1, out=torch.full((7, 8, 64), 7.0, device="cuda"))
+    assert status == gqa.STATUS_GROUP_RANGE
+    assert torch.equal(out[:5], good[:5]) and (out[5:] == 7).all()
+
+
+def test_captured_and_replayed():
+    x = make([5, 70], [400, 333], (64, 8, 128), torch.bfloat16)
+    want, _ = run(x, 0.1)
+    q, k, v = x["q"].cuda(), x["k"].cuda(), x["v"].cuda()
+    states = torch.tensor(x["states"], dtype=torch.int32, device="cuda")
+    starts = torch.tensor(x["starts"], dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = gqa.cross_attend(q, k, v, states, starts, 0.1)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_far_rows():
+    """States whose offsets pass 32 bits."""
+    E, S, H_kv, d = 33, 65536, 8, 128  # 33 * 65536 * 1024 elements: over 2^31
+    k = torch.zeros((E, S, H_kv, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k[-1, -200:].normal_(generator=g)
+    v[-1, -200:].normal_(generator=g)
+    q = torch.empty((3, 8, d), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    states = torch.zeros(E, dtype=torch.int32, device="cuda")
+    states[-1] = S
+    starts = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    starts[-1] = 3
+    out = gqa.cross_attend(q, k, v, states, starts, 0.3)
+    bound = tolerance(q, [k[-1, -200:]], [v[-1, -200:]], 0.3, S)
+    for i in range(3):
+        assert float((out[i].double() - attend64(q[i], k[-1], v[-1], 0.3)).abs().max()) <= bound
