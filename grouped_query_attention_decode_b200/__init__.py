@@ -39,7 +39,9 @@ EXPORTED = ("gqa_kv_append", "gqa_decode_workspace_size", "gqa_decode", "gqa_sta
             "gqa_kv_append_fp8", "gqa_kv_append_paged_fp8", "gqa_decode_fp8",
             "gqa_decode_paged_fp8", "gqa_kv_append_decode",
             "gqa_decode_shared_workspace_size", "gqa_decode_shared", "gqa_decode_shared_paged",
-            "gqa_cross_attend_workspace_size", "gqa_cross_attend")
+            "gqa_cross_attend_workspace_size", "gqa_cross_attend", "gqa_pages_workspace_size",
+            "gqa_pages_fork", "gqa_pages_free", "gqa_pages_reserve", "gqa_pages_compact",
+            "gqa_pages_copy")
 
 
 class GQAError(RuntimeError):
@@ -125,6 +127,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gqa_cross_attend.argtypes = [vp, vp, vp, i32p, i32p, c_int, c_int, c_int, c_int, c_int, c_int,
                                      c_float, c_int, vp, vp, c_size, i32p, vp]
     lib.gqa_cross_attend.restype = c_int
+    lib.gqa_pages_workspace_size.argtypes = [c_int]
+    lib.gqa_pages_workspace_size.restype = c_size
+    lib.gqa_pages_fork.argtypes = [i32p, i32p, i32p, c_int, i32p, i32p, c_int, c_int, i32p, c_int,
+                                   i32p, vp]
+    lib.gqa_pages_fork.restype = c_int
+    lib.gqa_pages_free.argtypes = [i32p, c_int, i32p, i32p, c_int, c_int, i32p, c_int, i32p, vp]
+    lib.gqa_pages_free.restype = c_int
+    lib.gqa_pages_reserve.argtypes = [i32p, i32p, c_int, c_int, c_int, c_int, i32p, c_int, i32p, vp,
+                                      c_size, i32p, vp]
+    lib.gqa_pages_reserve.restype = c_int
+    lib.gqa_pages_compact.argtypes = [i32p, c_int, c_int, i32p, c_int, i32p, i32p, vp, c_size, i32p,
+                                      vp]
+    lib.gqa_pages_compact.restype = c_int
+    lib.gqa_pages_copy.argtypes = [vp, vp, i32p, c_int, c_int, c_int, c_int, c_int, c_int, i32p, vp]
+    lib.gqa_pages_copy.restype = c_int
     lib.gqa_status_string.argtypes = [c_int]
     lib.gqa_status_string.restype = ctypes.c_char_p
     lib.gqa_set_wait_timeout_ns.argtypes = [ctypes.c_ulonglong]
@@ -548,3 +565,94 @@ def cross_attend(q, k_enc, v_enc, enc_lens, q_start, scale: float, out=None, wor
             S_max, float(scale), dtype, _ptr(out), _ptr(workspace), workspace.numel(),
             _ptr(status), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------ pages that sequences share
+def _pages_workspace(n_pages: int, workspace, like, stream):
+    n = int(load_library().gqa_pages_workspace_size(n_pages))
+    return _made(torch.empty(n, dtype=torch.uint8, device=like.device), stream) if workspace is None else workspace
+
+
+def pages_fork(parents, table_in, lens_in, table_out, lens_out, ref_counts, status=None, stream=None) -> None:
+    """gqa_pages_fork: sequence i of (table_out, lens_out) becomes a copy of sequence parents[i] of
+    (table_in, lens_in), -1: empty; ref_counts [n_pages] follows."""
+    (B_in, max_pages), B_out = table_in.shape, table_out.shape[0]
+    n_pages = ref_counts.shape[0]
+    _i32(table_in, (B_in, max_pages), "table_in"), _i32(table_out, (B_out, max_pages), "table_out")
+    _i32(lens_in, (B_in,), "lens_in"), _i32(lens_out, (B_out,), "lens_out")
+    _i32(parents, (B_out,), "parents"), _i32(ref_counts, (n_pages,), "ref_counts")
+    stream = _on(stream, table_in, parents, lens_in, table_out, lens_out, ref_counts, status)
+    with _Device(table_in):
+        _check(load_library().gqa_pages_fork(
+            _ptr(parents), _ptr(table_in), _ptr(lens_in), B_in, _ptr(table_out), _ptr(lens_out), B_out,
+            max_pages, _ptr(ref_counts), n_pages, _ptr(status), _stream(stream)))
+
+
+def pages_free(seqs, block_table, seq_lens, ref_counts, status=None, stream=None) -> None:
+    """gqa_pages_free: empty the sequences listed in ``seqs`` (int32 [n])."""
+    B, max_pages = block_table.shape
+    n_pages = ref_counts.shape[0]
+    _i32(seqs, (seqs.numel(),), "seqs"), _i32(block_table, (B, max_pages), "block_table")
+    _i32(seq_lens, (B,), "seq_lens"), _i32(ref_counts, (n_pages,), "ref_counts")
+    stream = _on(stream, block_table, seqs, seq_lens, ref_counts, status)
+    with _Device(block_table):
+        _check(load_library().gqa_pages_free(
+            _ptr(seqs), seqs.numel(), _ptr(block_table), _ptr(seq_lens), B, max_pages, _ptr(ref_counts),
+            n_pages, _ptr(status), _stream(stream)))
+
+
+def pages_reserve(block_table, seq_lens, ref_counts, rows: int, page_size: int, copies=None,
+                  workspace=None, status=None, stream=None) -> torch.Tensor:
+    """gqa_pages_reserve: every sequence gets pages of its own for its next ``rows`` rows.  Returns
+    copies [B, 2] (old page, new page; -1: none), for pages_copy."""
+    B, max_pages = block_table.shape
+    n_pages = ref_counts.shape[0]
+    _i32(block_table, (B, max_pages), "block_table"), _i32(seq_lens, (B,), "seq_lens")
+    _i32(ref_counts, (n_pages,), "ref_counts")
+    stream = _on(stream, block_table, seq_lens, ref_counts, copies, workspace, status)
+    with _Device(block_table):
+        if copies is None:
+            copies = _made(torch.empty((B, 2), dtype=torch.int32, device=block_table.device), stream)
+        _i32(copies, (B, 2), "copies")
+        workspace = _pages_workspace(n_pages, workspace, block_table, stream)
+        _check(load_library().gqa_pages_reserve(
+            _ptr(block_table), _ptr(seq_lens), B, max_pages, int(page_size), int(rows), _ptr(ref_counts),
+            n_pages, _ptr(copies), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+    return copies
+
+
+def pages_compact(block_table, ref_counts, copies=None, n_live=None, workspace=None, status=None,
+                  stream=None):
+    """gqa_pages_compact: the pages in use take the lowest numbers.  Returns (copies
+    [max(1, n_pages // 2), 2], n_live [1]); run pages_copy on the copies."""
+    B, max_pages = block_table.shape
+    n_pages = ref_counts.shape[0]
+    _i32(block_table, (B, max_pages), "block_table"), _i32(ref_counts, (n_pages,), "ref_counts")
+    stream = _on(stream, block_table, ref_counts, copies, n_live, workspace, status)
+    with _Device(block_table):
+        if copies is None:
+            copies = _made(torch.empty((max(1, n_pages // 2), 2), dtype=torch.int32, device=block_table.device), stream)
+        if n_live is None:
+            n_live = _made(torch.empty(1, dtype=torch.int32, device=block_table.device), stream)
+        _i32(copies, (max(1, n_pages // 2), 2), "copies"), _i32(n_live, (1,), "n_live")
+        workspace = _pages_workspace(n_pages, workspace, block_table, stream)
+        _check(load_library().gqa_pages_compact(
+            _ptr(block_table), B, max_pages, _ptr(ref_counts), n_pages, _ptr(copies), _ptr(n_live),
+            _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+    return copies, n_live
+
+
+def pages_copy(k_pool, v_pool, copies, status=None, stream=None) -> None:
+    """gqa_pages_copy: carry out ``copies`` [n, 2] (from, to) in the pools of one layer,
+    [n_pages, page_size, H_kv, d] of bfloat16, float32 or e4m3 codes."""
+    if k_pool.dtype in _DTYPES:
+        dtype = _DTYPES[k_pool.dtype]
+    else:
+        k_pool, v_pool, dtype = _codes(k_pool), _codes(v_pool), DTYPE_E4M3
+    n_pages, page_size, H_kv, d = k_pool.shape
+    _same(v_pool, k_pool.shape, k_pool.dtype, "v_pool"), _i32(copies, (copies.shape[0], 2), "copies")
+    stream = _on(stream, k_pool, v_pool, copies, status)
+    with _Device(k_pool):
+        _check(load_library().gqa_pages_copy(
+            _ptr(k_pool), _ptr(v_pool), _ptr(copies), copies.shape[0], page_size, n_pages, H_kv, d,
+            dtype, _ptr(status), _stream(stream)))

@@ -218,6 +218,8 @@ extern "C" size_t gqa_decode_multi_workspace_size(int B, int Q, int H_q, int H_k
     return geometry(B, H_q, H_kv, d, sms, Q).bytes;
 }
 
+int gqa::device_sm_count(int *dev_out) { return current_sm_count(dev_out); }
+
 size_t gqa::decode_counter_region(int B, int H_q, int H_kv, int d, size_t *offset) {
     if (check_shape(B, H_q, H_kv, d, 1, GQA_DTYPE_BF16) != GQA_OK) return 0;
     int dev = 0;

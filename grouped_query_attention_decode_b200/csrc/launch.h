@@ -12,6 +12,10 @@ namespace gqa {
 
 struct DecodeParams;
 
+// SM count of the current device (its number in *dev_out), or <= 0 when there is none or it is
+// not sm_100.
+int device_sm_count(int *dev_out);
+
 // TMA descriptors of one bf16 decode call: q as [B*H_q rows][d], the caches as
 // (d, H_kv, L_max, B) with 128-row and 8-row boxes of 64 columns, all with 128-byte swizzle.
 struct TmaMaps {

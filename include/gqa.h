@@ -85,8 +85,9 @@ typedef enum {
 #define GQA_STATUS_GROUP_RANGE 32     /* gqa_decode_shared*, gqa_cross_attend: a group's start is
                                          negative, past its end, or past the batch; the group
                                          shares nothing (its tokens' outputs are not valid) */
-#define GQA_STATUS_PAGE_REFS 64       /* gqa_pages_*: a page's count of holders would fall below
-                                         zero; it is left at zero */
+#define GQA_STATUS_PAGE_REFS 64       /* gqa_pages_*: a page's count of holders fell below zero, or
+                                         a held page has a count of zero: the counts do not belong
+                                         to the tables */
 #define GQA_STATUS_POOL_FULL 128      /* gqa_pages_reserve: not enough free pages; the sequences
                                          from the first that found none on got nothing */
 #define GQA_STATUS_INDEX_RANGE 256    /* gqa_pages_*: a sequence or page number in an argument is
@@ -359,6 +360,67 @@ int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const 
                      const int32_t *q_start, int E, int N, int H_q, int H_kv, int d, int S_max,
                      float scale, gqa_dtype_t dtype, float *out, void *workspace,
                      size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
+/*
+ * Pages that several sequences hold.  "GQA 阅读笔记" (the vLLM PagedAttention paragraph: fixed-size
+ * blocks) says that the cache is managed in pages; these calls manage them on the device, without
+ * a host round trip.  The state, all int32 on the device and the caller's:
+ *   block_table [B][max_pages]  pages of each sequence in order, -1 where it holds none
+ *   seq_lens    [B]
+ *   ref_counts  [n_pages]       table entries that hold each page; 0: the page is free.  16-byte
+ *                               aligned for gqa_pages_reserve and gqa_pages_compact
+ * An empty pool is counts of zero and tables of -1.  One table serves every layer of a model: the
+ * calls below that move pages write the moves down as pairs (from, to), and gqa_pages_copy
+ * carries them out in one layer's pools.  Every result is determined by the inputs (free pages
+ * are taken lowest number first).  A table entry outside [-1, n_pages) counts as -1 and sets
+ * GQA_STATUS_PAGE_RANGE; counts that do not belong to the tables set GQA_STATUS_PAGE_REFS where
+ * that is noticed.
+ *
+ * gqa_pages_fork: table_out[i] = table_in[parents[i]], lens_out[i] = lens_in[parents[i]] for i <
+ *   B_out, and the counts of the pages follow: samples of one prompt, or the beams of a search
+ *   taking their parents' rows.  parents[i] = -1 leaves sequence i empty.  Sequences that nobody
+ *   takes as a parent are freed; afterwards table_out is the state and table_in is not.  Input and
+ *   output arrays must not overlap (GQA_ERR_OVERLAP).  A parent outside [-1, B_in) counts as -1
+ *   and sets GQA_STATUS_INDEX_RANGE.
+ * gqa_pages_free: empties the n sequences listed in seqs (a sequence listed twice is freed once;
+ *   a number outside [0, B) is skipped, GQA_STATUS_INDEX_RANGE).
+ * gqa_pages_reserve: gives every sequence pages of its own for its next `rows` rows, [seq_lens[b],
+ *   seq_lens[b] + rows): a new page where it has none, and in the place of a page that others hold
+ *   too (copy on write) -- except that when every holder is about to write it, the last of them
+ *   keeps it.  copies [B][2] gets (old, new) where rows of the old page have to be copied, else
+ *   (-1, -1): run gqa_pages_copy on it before appending.  The lengths do not change.  A sequence
+ *   whose rows do not fit max_pages * page_size gets nothing (GQA_STATUS_APPEND_OVERFLOW).  When
+ *   free pages run out, the first sequence that they do not suffice for and those behind it that
+ *   need any get none (GQA_STATUS_POOL_FULL); appending to such a sequence would write a shared
+ *   page, so check the status, or the counts, before.
+ * gqa_pages_compact: moves the pages in use to the front of the pool.  With n of them, the pages
+ *   numbered n and up, in ascending order, take the places of the free ones below n; tables and
+ *   counts follow, copies [max(1, n_pages / 2)][2] gets the moves, (-1, -1) behind the last, and
+ *   n_live [1] gets n.
+ * gqa_pages_copy: copies page from to page to in k_pool and v_pool [n_pages][page_size][H_kv][d]
+ *   for each of the n pairs; (-1, -1) is skipped, another pair outside the pool too, with
+ *   GQA_STATUS_INDEX_RANGE.  The pages written must be distinct and not among those read.  Any
+ *   dtype, GQA_DTYPE_E4M3 included.
+ * The workspace of gqa_pages_reserve and gqa_pages_compact needs gqa_pages_workspace_size() bytes,
+ * 256-byte aligned, and no zero-fill.
+ */
+size_t gqa_pages_workspace_size(int n_pages);
+int gqa_pages_fork(const int32_t *parents, const int32_t *table_in, const int32_t *lens_in, int B_in,
+                   int32_t *table_out, int32_t *lens_out, int B_out, int max_pages,
+                   int32_t *ref_counts, int n_pages, int32_t *status, cudaStream_t stream);
+int gqa_pages_free(const int32_t *seqs, int n, int32_t *block_table, int32_t *seq_lens, int B,
+                   int max_pages, int32_t *ref_counts, int n_pages, int32_t *status,
+                   cudaStream_t stream);
+int gqa_pages_reserve(int32_t *block_table, const int32_t *seq_lens, int B, int max_pages,
+                      int page_size, int rows, int32_t *ref_counts, int n_pages, int32_t *copies,
+                      void *workspace, size_t workspace_bytes, int32_t *status,
+                      cudaStream_t stream);
+int gqa_pages_compact(int32_t *block_table, int B, int max_pages, int32_t *ref_counts, int n_pages,
+                      int32_t *copies, int32_t *n_live, void *workspace, size_t workspace_bytes,
+                      int32_t *status, cudaStream_t stream);
+int gqa_pages_copy(void *k_pool, void *v_pool, const int32_t *copies, int n, int page_size,
+                   int n_pages, int H_kv, int d, gqa_dtype_t dtype, int32_t *status,
+                   cudaStream_t stream);
 
 /*
  * gqa_decode_noalloc: gqa_decode without a caller-provided workspace.  (The pages have no
