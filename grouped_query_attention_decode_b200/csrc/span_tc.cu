@@ -185,7 +185,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
     uint8_t *const ring = smem + 2 * C::TILE_BYTES;
     using Small = typename C::Small;
     auto *const sm = reinterpret_cast<Small *>(ring + S * C::TILE_BYTES);
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);  // the same in all lanes, and known to be
     const int lane = threadIdx.x & 31;
 
     if ((smem_u32(smem) & 1023u) != 0) {
@@ -280,35 +280,18 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
             const bool pair = pc.pair;
             const int jj0 = (x ^ z0) & 1;  // this stream's first step of the piece
             z0 ^= steps & 1;
-            int token;
-            const long long orow = span_row(p, g, pair ? jj0 : 0, row, token);
-            const bool busy = __any_sync(kFullMask, orow >= 0);  // warps of padding rows only keep the barriers going
-            const bool both = !pair && steps >= 2;               // the streams share the rows
-            const bool whole = g.whole();
+            const bool both = !pair && steps >= 2;  // the streams share the rows
             // visible columns of the stream's first tile, and how many fewer from one step of the
             // stream to the next; padding rows hold anything
-            int left = (orow >= 0 ? seen_rows(p, g, token) : 1 << 30) - (g.j0 + (pair ? 0 : jj0)) * T;
-            const int fewer = pair ? T : 2 * T;
-            float *dst = nullptr, *dst_ml = nullptr;
-            if (orow >= 0) {
-                if (!whole) {
-                    float *slot = p.slots + (2ll * blockIdx.x + (g.first ? 0 : 1)) * p.slot_floats;
-                    const int srow = (pair ? jj0 : 0) * C::RT + row;
-                    dst = slot + srow * D;
-                    dst_ml = slot + p.unit_rows * D + 2 * srow;
-                } else if (p.B > 0) {
-                    const long long rr = (g.s < p.P ? 0 : static_cast<long long>(p.N) * p.H_q) + orow;
-                    dst = p.res + rr * D;
-                    dst_ml = p.res_ml + 2 * rr;
-                } else {
-                    dst = p.out + orow * D;
-                }
+            int left = 1 << 30;
+            {
+                int token;
+                if (span_row(p, g, pair ? jj0 : 0, row, token) >= 0) left = seen_rows(p, g, token) - (g.j0 + (pair ? 0 : jj0)) * T;
             }
-            // the piece's fields are in registers now
-            __syncwarp();
-            if (lane == 0) pieces.release(i);
+            const bool busy = __any_sync(kFullMask, left < 1 << 30);  // warps of padding rows only keep the barriers going
+            const int fewer = pair ? T : 2 * T;
             float m = -INFINITY;
-            float2 l2 = make_float2(0.f, 0.f);
+            float2 l2[2] = {};
 #pragma unroll
             for (int e = 0; e < D / 2; ++e) o2[e] = make_float2(0.f, 0.f);
             for (int jj = jj0; jj < steps; jj += 2, left -= fewer) {
@@ -322,21 +305,24 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 if (busy) {
                     tc_fence_after_sync();
                     const bool cut = __any_sync(kFullMask, left < T);
-                    // The scores are read twice, 32 columns at a time: beside the sums there is no room
-                    // for a whole row of them.
+                    // The scores are read twice: beside the sums there is no room for a whole row.
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int c = 0; c < T; c += 32) {
-                        uint32_t a[32];
+                    for (int c = 0; c < T; c += 64) {
+                        uint32_t a[64];
                         tmem_ld32(st + c, a);
+                        tmem_ld32(st + c + 32, a + 32);
                         tmem_wait_ld();
                         if (cut) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                            for (int e = 0; e < 64; ++e)
                                 if (c + e >= left) a[e] = 0xff800000u;  // -infinity
+                            tmem_st32(st + c, a);
+                            tmem_st32(st + c + 32, a + 32);
+                            tmem_wait_st();
                         }
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
+                        for (int e = 0; e < 64; e += 8)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(a[e + k]), __uint_as_float(a[e + 4 + k])));
@@ -353,7 +339,8 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                             m = m_new;
                         }
                         const float2 al2 = make_float2(alpha, alpha);
-                        l2 = mul_f32x2(l2, al2);
+                        l2[0] = mul_f32x2(l2[0], al2);
+                        l2[1] = mul_f32x2(l2[1], al2);
 #pragma unroll
                         for (int e = 0; e < D / 2; ++e) o2[e] = mul_f32x2(o2[e], al2);
                     }
@@ -364,11 +351,6 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                         uint32_t a[32];
                         tmem_ld32(st + c, a);
                         tmem_wait_ld();
-                        if (cut) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (c + e >= left) a[e] = 0xff800000u;
-                        }
 #pragma unroll
                         for (int b = 0; b < 32; b += 16) {
                             uint32_t hl[16];
@@ -376,11 +358,12 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                             for (int e = 0; e < 16; e += 2) {
                                 const float2 t = fma_f32x2(make_float2(__uint_as_float(a[b + e]), __uint_as_float(a[b + e + 1])), sc2, ref2);
                                 const float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-                                l2 = add_f32x2(l2, pr);
+                                l2[(e >> 1) & 1] = add_f32x2(l2[(e >> 1) & 1], pr);
                                 const __nv_bfloat162 hi = __floats2bfloat162_rn(pr.x, pr.y);
                                 const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hi);
                                 // what the rounding left, exact in fp32
-                                const __nv_bfloat162 lo = __floats2bfloat162_rn(pr.x - __uint_as_float(hb << 16), pr.y - __uint_as_float(hb & 0xffff0000u));
+                                const float2 left2 = fma_f32x2(make_float2(__uint_as_float(hb << 16), __uint_as_float(hb & 0xffff0000u)), make_float2(-1.f, -1.f), pr);
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(left2.x, left2.y);
                                 hl[e / 2] = hb;
                                 hl[8 + e / 2] = *reinterpret_cast<const uint32_t *>(&lo);
                             }
@@ -394,11 +377,15 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 if (lane == 0) mbar_arrive(&sm->p_full[x]);
             }
             if (!ok) break;
-            if (jj0 >= steps) continue;  // a piece of one step is the other stream's
+            if (jj0 >= steps) {  // a piece of one step is the other stream's
+                __syncwarp();
+                if (lane == 0) pieces.release(i);
+                continue;
+            }
             // -------- the piece ends: sums, m, l to where they belong
             ok = take_o(busy);
             if (!ok) break;
-            float l = l2.x + l2.y;
+            float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
             int c0 = 0, c1 = D;
             if (both && busy) {
                 // The streams share the rows.  Each finishes half of the columns and leaves the other
@@ -451,6 +438,27 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 c0 = x * (D / 2);
                 c1 = c0 + D / 2;
             }
+            // Where the row goes: looked up again, the registers being short meanwhile.
+            int token;
+            const long long orow = span_row(p, g, pair ? jj0 : 0, row, token);
+            const bool whole = g.whole();
+            float *dst = nullptr, *dst_ml = nullptr;
+            if (orow >= 0) {
+                if (!whole) {
+                    float *slot = p.slots + (2ll * blockIdx.x + (g.first ? 0 : 1)) * p.slot_floats;
+                    const int srow = (pair ? jj0 : 0) * C::RT + row;
+                    dst = slot + srow * D;
+                    dst_ml = slot + p.unit_rows * D + 2 * srow;
+                } else if (p.B > 0) {
+                    const long long rr = (g.s < p.P ? 0 : static_cast<long long>(p.N) * p.H_q) + orow;
+                    dst = p.res + rr * D;
+                    dst_ml = p.res_ml + 2 * rr;
+                } else {
+                    dst = p.out + orow * D;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) pieces.release(i);
             if (dst != nullptr) {
                 if (dst_ml != nullptr && c0 == 0) *reinterpret_cast<float2 *>(dst_ml) = make_float2(m, l);
                 const float norm = whole && p.B == 0 ? 1.f / l : 1.f;
@@ -543,7 +551,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ UMMA issuer
-        if (lane == 0) {
+        if (elect_one()) {
             // K and q: K-major, 8-row groups 1024 B apart.  V: MN-major (d by rows), its 64-column
             // blocks T * 128 B apart.
             const uint64_t dk0 = sdesc_sw128(smem_u32(ring), 16, 1024);
