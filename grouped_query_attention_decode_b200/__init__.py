@@ -9,6 +9,7 @@ the binding's functions raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -426,62 +427,70 @@ def decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
 
 
 # ------------------------------------------------------------------ rows that sequences share
-def _on(stream, first: torch.Tensor, *tensors):
-    """The stream of a call on ``first``'s device.  Every tensor has to be on that device.  A
-    tensor the binding allocates for the call (on the device's current stream) and the call then
-    uses on another stream is kept from reuse until that stream is done with it (_made)."""
-    for t in tensors:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    if not first.is_cuda:
+# Small calls are bound by the host, so what follows makes few Python calls per argument.
+def _tensors(first: torch.Tensor, *tensors) -> int:
+    """The device number of ``first``; every tensor (None: absent) has to be dense and on it."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("libgqa needs CUDA tensors")
-    return torch.cuda.current_stream(first.device) if stream is None else stream
+    if not first.is_contiguous():
+        raise ValueError("libgqa needs contiguous tensors")
+    for t in tensors:
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError(f"tensors on {first.device} and {t.device}")
+            if not t.is_contiguous():
+                raise ValueError("libgqa needs contiguous tensors")
+    return dev
+
+
+def _want(t: torch.Tensor, shape, dtype, name: str) -> None:
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _made(t: torch.Tensor, stream) -> torch.Tensor:
-    if stream != torch.cuda.current_stream(t.device):
-        stream.wait_stream(torch.cuda.current_stream(t.device))  # earlier users of the memory
-        t.record_stream(stream)
+    """A tensor that the binding allocated (on its device's current stream) for a call on
+    ``stream``: its memory's earlier users come first, and it is not given away before the call is
+    done."""
+    if stream is not None:
+        current = torch.cuda.current_stream(t.device)
+        if stream != current:
+            stream.wait_stream(current)
+            t.record_stream(stream)
     return t
 
 
-class _Device:
-    """The CUDA device that the library works on is the current one: make it the tensors'."""
-
-    def __init__(self, t: torch.Tensor):
-        self.want = t.device.index
-        self.had = torch.cuda.current_device()
-
-    def __enter__(self):
-        if self.had != self.want:
-            torch.cuda.set_device(self.want)
-
-    def __exit__(self, *exc):
-        if self.had != self.want:
-            torch.cuda.set_device(self.had)
+def _run(dev: int, fn, *args) -> None:
+    """fn(*args) with the tensors' device as the current one, which is the library's."""
+    if torch.cuda.current_device() == dev:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args))
 
 
-def _i32(t: torch.Tensor, shape, name: str) -> torch.Tensor:
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be int32 {list(shape)}, not {t.dtype} {list(t.shape)}")
-    return t
-
-
-def _same(t: torch.Tensor, shape, dtype, name: str) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    return t
-
-
-def _out_and_workspace(q, out, workspace, n: int, stream):
+@functools.lru_cache(maxsize=1024)
+def _bytes_on(dev: int, fn: str, *sizes) -> int:
+    with torch.cuda.device(dev):
+        n = int(getattr(load_library(), fn)(*sizes))
     if n == 0:
         raise GQAError(-9, "no usable sm_100 device is current, or invalid sizes")
-    if out is None:
-        out = _made(torch.empty(q.shape, dtype=torch.float32, device=q.device), stream)
-    _same(out, q.shape, torch.float32, "out")
+    return n
+
+
+def _workspace(q: torch.Tensor, dev: int, workspace, stream, fn: str, *sizes) -> torch.Tensor:
     if workspace is None:
-        workspace = _made(torch.empty(n, dtype=torch.uint8, device=q.device), stream)
-    return out, workspace
+        workspace = _made(torch.empty(_bytes_on(dev, fn, *sizes), dtype=torch.uint8, device=q.device), stream)
+    return workspace
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def shared_workspace_size(B: int, Q: int, P: int, H_q: int, H_kv: int, d: int, dtype: torch.dtype) -> int:
@@ -495,22 +504,28 @@ def decode_shared(q, k_prefix, v_prefix, prefix_lens, group_start, k_cache, v_ca
     rows of k_prefix[g], read once for all of them, and then their own seq_lens[b] rows.  q is
     [B, H_q, d], or [B, Q, H_q, d] for Q query tokens per sequence; returns out of q's shape,
     float32."""
-    q4 = q if q.dim() == 4 else q.unsqueeze(1)
-    B, Q, H_q, d = q4.shape
+    lib = _lib or load_library()
+    shape, dtype = q.shape, q.dtype
+    B, Q, H_q, d = shape if len(shape) == 4 else (shape[0], 1, *shape[1:])
     P, L_prefix, H_kv, _ = k_prefix.shape
     L_max = k_cache.shape[1]
-    dtype = _dtype(q)
-    for t, n, shape in ((k_prefix, "k_prefix", (P, L_prefix, H_kv, d)), (v_prefix, "v_prefix", (P, L_prefix, H_kv, d)),
-                        (k_cache, "k_cache", (B, L_max, H_kv, d)), (v_cache, "v_cache", (B, L_max, H_kv, d))):
-        _same(t, shape, q.dtype, n)
-    _i32(prefix_lens, (P,), "prefix_lens"), _i32(group_start, (P + 1,), "group_start"), _i32(seq_lens, (B,), "seq_lens")
-    stream = _on(stream, q, k_prefix, v_prefix, prefix_lens, group_start, k_cache, v_cache, seq_lens, out, workspace, status)
-    with _Device(q):
-        out, workspace = _out_and_workspace(q, out, workspace, shared_workspace_size(B, Q, P, H_q, H_kv, d, q.dtype), stream)
-        _check(load_library().gqa_decode_shared(
-            _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_lens), _ptr(group_start), P, L_prefix,
-            _ptr(k_cache), _ptr(v_cache), _ptr(seq_lens), B, Q, H_q, H_kv, d, L_max, float(scale),
-            dtype, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+    code = _dtype(q)
+    _want(k_prefix, (P, L_prefix, H_kv, d), dtype, "k_prefix")
+    _want(v_prefix, (P, L_prefix, H_kv, d), dtype, "v_prefix")
+    _want(k_cache, (B, L_max, H_kv, d), dtype, "k_cache")
+    _want(v_cache, (B, L_max, H_kv, d), dtype, "v_cache")
+    _want(prefix_lens, (P,), torch.int32, "prefix_lens")
+    _want(group_start, (P + 1,), torch.int32, "group_start")
+    _want(seq_lens, (B,), torch.int32, "seq_lens")
+    dev = _tensors(q, k_prefix, v_prefix, prefix_lens, group_start, k_cache, v_cache, seq_lens, out, workspace, status)
+    if out is None:
+        out = _made(torch.empty_like(q, dtype=torch.float32), stream)
+    else:
+        _want(out, shape, torch.float32, "out")
+    workspace = _workspace(q, dev, workspace, stream, "gqa_decode_shared_workspace_size", B, Q, P, H_q, H_kv, d, code)
+    _run(dev, lib.gqa_decode_shared, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), prefix_lens.data_ptr(),
+         group_start.data_ptr(), P, L_prefix, k_cache.data_ptr(), v_cache.data_ptr(), seq_lens.data_ptr(), B, Q, H_q, H_kv, d,
+         L_max, scale, code, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(stream, dev))
     return out
 
 
@@ -519,24 +534,28 @@ def decode_shared_paged(q, k_pool, v_pool, block_table, seq_lens, group_start, s
     """gqa_decode_shared_paged: decode_paged for sequences [group_start[g], group_start[g+1]) whose
     first shared_rows[g] rows lie in the same pages, which are read once for all of them.  q is
     [B, H_q, d] or [B, Q, H_q, d]; returns out of q's shape, float32."""
-    q4 = q if q.dim() == 4 else q.unsqueeze(1)
-    B, Q, H_q, d = q4.shape
+    lib = _lib or load_library()
+    shape, dtype = q.shape, q.dtype
+    B, Q, H_q, d = shape if len(shape) == 4 else (shape[0], 1, *shape[1:])
     n_pages, page_size, H_kv, _ = k_pool.shape
     max_pages = block_table.shape[1]
     P = shared_rows.shape[0]
-    dtype = _dtype(q)
-    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        _same(t, (n_pages, page_size, H_kv, d), q.dtype, n)
-    _i32(block_table, (B, max_pages), "block_table"), _i32(seq_lens, (B,), "seq_lens")
-    _i32(group_start, (P + 1,), "group_start"), _i32(shared_rows, (P,), "shared_rows")
-    stream = _on(stream, q, k_pool, v_pool, block_table, seq_lens, group_start, shared_rows, out, workspace, status)
-    with _Device(q):
-        out, workspace = _out_and_workspace(q, out, workspace, shared_workspace_size(B, Q, P, H_q, H_kv, d, q.dtype), stream)
-        _check(load_library().gqa_decode_shared_paged(
-            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), max_pages, _ptr(seq_lens),
-            _ptr(group_start), _ptr(shared_rows), P, B, Q, H_q, H_kv, d, page_size, n_pages,
-            float(scale), dtype, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(status),
-            _stream(stream)))
+    code = _dtype(q)
+    _want(k_pool, (n_pages, page_size, H_kv, d), dtype, "k_pool")
+    _want(v_pool, (n_pages, page_size, H_kv, d), dtype, "v_pool")
+    _want(block_table, (B, max_pages), torch.int32, "block_table")
+    _want(seq_lens, (B,), torch.int32, "seq_lens")
+    _want(group_start, (P + 1,), torch.int32, "group_start")
+    _want(shared_rows, (P,), torch.int32, "shared_rows")
+    dev = _tensors(q, k_pool, v_pool, block_table, seq_lens, group_start, shared_rows, out, workspace, status)
+    if out is None:
+        out = _made(torch.empty_like(q, dtype=torch.float32), stream)
+    else:
+        _want(out, shape, torch.float32, "out")
+    workspace = _workspace(q, dev, workspace, stream, "gqa_decode_shared_workspace_size", B, Q, P, H_q, H_kv, d, code)
+    _run(dev, lib.gqa_decode_shared_paged, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), max_pages,
+         seq_lens.data_ptr(), group_start.data_ptr(), shared_rows.data_ptr(), P, B, Q, H_q, H_kv, d, page_size, n_pages, scale,
+         code, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(stream, dev))
     return out
 
 
@@ -551,73 +570,78 @@ def cross_attend(q, k_enc, v_enc, enc_lens, q_start, scale: float, out=None, wor
     """gqa_cross_attend: tokens [q_start[e], q_start[e+1]) of q [N, H_q, d] attend the states
     [0, enc_lens[e]) of k_enc, v_enc [E, S_max, H_kv, d].  Returns out [N, H_q, d] float32; tokens
     before q_start[0] or from q_start[E] on are left as they were in ``out``."""
-    N, H_q, d = q.shape
+    lib = _lib or load_library()
+    shape, dtype = q.shape, q.dtype
+    N, H_q, d = shape
     E, S_max, H_kv, _ = k_enc.shape
-    dtype = _dtype(q)
-    for t, n in ((k_enc, "k_enc"), (v_enc, "v_enc")):
-        _same(t, (E, S_max, H_kv, d), q.dtype, n)
-    _i32(enc_lens, (E,), "enc_lens"), _i32(q_start, (E + 1,), "q_start")
-    stream = _on(stream, q, k_enc, v_enc, enc_lens, q_start, out, workspace, status)
-    with _Device(q):
-        out, workspace = _out_and_workspace(q, out, workspace, cross_workspace_size(E, N, H_q, H_kv, d, q.dtype), stream)
-        _check(load_library().gqa_cross_attend(
-            _ptr(q), _ptr(k_enc), _ptr(v_enc), _ptr(enc_lens), _ptr(q_start), E, N, H_q, H_kv, d,
-            S_max, float(scale), dtype, _ptr(out), _ptr(workspace), workspace.numel(),
-            _ptr(status), _stream(stream)))
+    code = _dtype(q)
+    _want(k_enc, (E, S_max, H_kv, d), dtype, "k_enc")
+    _want(v_enc, (E, S_max, H_kv, d), dtype, "v_enc")
+    _want(enc_lens, (E,), torch.int32, "enc_lens")
+    _want(q_start, (E + 1,), torch.int32, "q_start")
+    dev = _tensors(q, k_enc, v_enc, enc_lens, q_start, out, workspace, status)
+    if out is None:
+        out = _made(torch.empty_like(q, dtype=torch.float32), stream)
+    else:
+        _want(out, shape, torch.float32, "out")
+    workspace = _workspace(q, dev, workspace, stream, "gqa_cross_attend_workspace_size", E, N, H_q, H_kv, d, code)
+    _run(dev, lib.gqa_cross_attend, q.data_ptr(), k_enc.data_ptr(), v_enc.data_ptr(), enc_lens.data_ptr(), q_start.data_ptr(), E, N,
+         H_q, H_kv, d, S_max, scale, code, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status),
+         _raw_stream(stream, dev))
     return out
 
 
 # ------------------------------------------------------------------ pages that sequences share
-def _pages_workspace(n_pages: int, workspace, like, stream):
-    n = int(load_library().gqa_pages_workspace_size(n_pages))
-    return _made(torch.empty(n, dtype=torch.uint8, device=like.device), stream) if workspace is None else workspace
-
-
 def pages_fork(parents, table_in, lens_in, table_out, lens_out, ref_counts, status=None, stream=None) -> None:
     """gqa_pages_fork: sequence i of (table_out, lens_out) becomes a copy of sequence parents[i] of
     (table_in, lens_in), -1: empty; ref_counts [n_pages] follows."""
+    lib = _lib or load_library()
     (B_in, max_pages), B_out = table_in.shape, table_out.shape[0]
     n_pages = ref_counts.shape[0]
-    _i32(table_in, (B_in, max_pages), "table_in"), _i32(table_out, (B_out, max_pages), "table_out")
-    _i32(lens_in, (B_in,), "lens_in"), _i32(lens_out, (B_out,), "lens_out")
-    _i32(parents, (B_out,), "parents"), _i32(ref_counts, (n_pages,), "ref_counts")
-    stream = _on(stream, table_in, parents, lens_in, table_out, lens_out, ref_counts, status)
-    with _Device(table_in):
-        _check(load_library().gqa_pages_fork(
-            _ptr(parents), _ptr(table_in), _ptr(lens_in), B_in, _ptr(table_out), _ptr(lens_out), B_out,
-            max_pages, _ptr(ref_counts), n_pages, _ptr(status), _stream(stream)))
+    _want(table_in, (B_in, max_pages), torch.int32, "table_in")
+    _want(table_out, (B_out, max_pages), torch.int32, "table_out")
+    _want(lens_in, (B_in,), torch.int32, "lens_in")
+    _want(lens_out, (B_out,), torch.int32, "lens_out")
+    _want(parents, (B_out,), torch.int32, "parents")
+    _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
+    dev = _tensors(table_in, parents, lens_in, table_out, lens_out, ref_counts, status)
+    _run(dev, lib.gqa_pages_fork, parents.data_ptr(), table_in.data_ptr(), lens_in.data_ptr(), B_in, table_out.data_ptr(),
+         lens_out.data_ptr(), B_out, max_pages, ref_counts.data_ptr(), n_pages, _addr(status), _raw_stream(stream, dev))
 
 
 def pages_free(seqs, block_table, seq_lens, ref_counts, status=None, stream=None) -> None:
     """gqa_pages_free: empty the sequences listed in ``seqs`` (int32 [n])."""
+    lib = _lib or load_library()
     B, max_pages = block_table.shape
-    n_pages = ref_counts.shape[0]
-    _i32(seqs, (seqs.numel(),), "seqs"), _i32(block_table, (B, max_pages), "block_table")
-    _i32(seq_lens, (B,), "seq_lens"), _i32(ref_counts, (n_pages,), "ref_counts")
-    stream = _on(stream, block_table, seqs, seq_lens, ref_counts, status)
-    with _Device(block_table):
-        _check(load_library().gqa_pages_free(
-            _ptr(seqs), seqs.numel(), _ptr(block_table), _ptr(seq_lens), B, max_pages, _ptr(ref_counts),
-            n_pages, _ptr(status), _stream(stream)))
+    n, n_pages = seqs.shape[0], ref_counts.shape[0]
+    _want(seqs, (n,), torch.int32, "seqs")
+    _want(block_table, (B, max_pages), torch.int32, "block_table")
+    _want(seq_lens, (B,), torch.int32, "seq_lens")
+    _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
+    dev = _tensors(block_table, seqs, seq_lens, ref_counts, status)
+    _run(dev, lib.gqa_pages_free, seqs.data_ptr(), n, block_table.data_ptr(), seq_lens.data_ptr(), B, max_pages,
+         ref_counts.data_ptr(), n_pages, _addr(status), _raw_stream(stream, dev))
 
 
 def pages_reserve(block_table, seq_lens, ref_counts, rows: int, page_size: int, copies=None,
                   workspace=None, status=None, stream=None) -> torch.Tensor:
     """gqa_pages_reserve: every sequence gets pages of its own for its next ``rows`` rows.  Returns
     copies [B, 2] (old page, new page; -1: none), for pages_copy."""
+    lib = _lib or load_library()
     B, max_pages = block_table.shape
     n_pages = ref_counts.shape[0]
-    _i32(block_table, (B, max_pages), "block_table"), _i32(seq_lens, (B,), "seq_lens")
-    _i32(ref_counts, (n_pages,), "ref_counts")
-    stream = _on(stream, block_table, seq_lens, ref_counts, copies, workspace, status)
-    with _Device(block_table):
-        if copies is None:
-            copies = _made(torch.empty((B, 2), dtype=torch.int32, device=block_table.device), stream)
-        _i32(copies, (B, 2), "copies")
-        workspace = _pages_workspace(n_pages, workspace, block_table, stream)
-        _check(load_library().gqa_pages_reserve(
-            _ptr(block_table), _ptr(seq_lens), B, max_pages, int(page_size), int(rows), _ptr(ref_counts),
-            n_pages, _ptr(copies), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+    _want(block_table, (B, max_pages), torch.int32, "block_table")
+    _want(seq_lens, (B,), torch.int32, "seq_lens")
+    _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
+    dev = _tensors(block_table, seq_lens, ref_counts, copies, workspace, status)
+    if copies is None:
+        copies = _made(torch.empty((B, 2), dtype=torch.int32, device=block_table.device), stream)
+    else:
+        _want(copies, (B, 2), torch.int32, "copies")
+    workspace = _workspace(block_table, dev, workspace, stream, "gqa_pages_workspace_size", n_pages)
+    _run(dev, lib.gqa_pages_reserve, block_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, page_size, rows,
+         ref_counts.data_ptr(), n_pages, copies.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status),
+         _raw_stream(stream, dev))
     return copies
 
 
@@ -625,34 +649,39 @@ def pages_compact(block_table, ref_counts, copies=None, n_live=None, workspace=N
                   stream=None):
     """gqa_pages_compact: the pages in use take the lowest numbers.  Returns (copies
     [max(1, n_pages // 2), 2], n_live [1]); run pages_copy on the copies."""
+    lib = _lib or load_library()
     B, max_pages = block_table.shape
     n_pages = ref_counts.shape[0]
-    _i32(block_table, (B, max_pages), "block_table"), _i32(ref_counts, (n_pages,), "ref_counts")
-    stream = _on(stream, block_table, ref_counts, copies, n_live, workspace, status)
-    with _Device(block_table):
-        if copies is None:
-            copies = _made(torch.empty((max(1, n_pages // 2), 2), dtype=torch.int32, device=block_table.device), stream)
-        if n_live is None:
-            n_live = _made(torch.empty(1, dtype=torch.int32, device=block_table.device), stream)
-        _i32(copies, (max(1, n_pages // 2), 2), "copies"), _i32(n_live, (1,), "n_live")
-        workspace = _pages_workspace(n_pages, workspace, block_table, stream)
-        _check(load_library().gqa_pages_compact(
-            _ptr(block_table), B, max_pages, _ptr(ref_counts), n_pages, _ptr(copies), _ptr(n_live),
-            _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+    _want(block_table, (B, max_pages), torch.int32, "block_table")
+    _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
+    dev = _tensors(block_table, ref_counts, copies, n_live, workspace, status)
+    most = max(1, n_pages // 2)
+    if copies is None:
+        copies = _made(torch.empty((most, 2), dtype=torch.int32, device=block_table.device), stream)
+    else:
+        _want(copies, (most, 2), torch.int32, "copies")
+    if n_live is None:
+        n_live = _made(torch.empty(1, dtype=torch.int32, device=block_table.device), stream)
+    else:
+        _want(n_live, (1,), torch.int32, "n_live")
+    workspace = _workspace(block_table, dev, workspace, stream, "gqa_pages_workspace_size", n_pages)
+    _run(dev, lib.gqa_pages_compact, block_table.data_ptr(), B, max_pages, ref_counts.data_ptr(), n_pages, copies.data_ptr(),
+         n_live.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status), _raw_stream(stream, dev))
     return copies, n_live
 
 
 def pages_copy(k_pool, v_pool, copies, status=None, stream=None) -> None:
     """gqa_pages_copy: carry out ``copies`` [n, 2] (from, to) in the pools of one layer,
     [n_pages, page_size, H_kv, d] of bfloat16, float32 or e4m3 codes."""
+    lib = _lib or load_library()
     if k_pool.dtype in _DTYPES:
-        dtype = _DTYPES[k_pool.dtype]
+        code = _DTYPES[k_pool.dtype]
     else:
-        k_pool, v_pool, dtype = _codes(k_pool), _codes(v_pool), DTYPE_E4M3
+        k_pool, v_pool, code = _codes(k_pool), _codes(v_pool), DTYPE_E4M3
     n_pages, page_size, H_kv, d = k_pool.shape
-    _same(v_pool, k_pool.shape, k_pool.dtype, "v_pool"), _i32(copies, (copies.shape[0], 2), "copies")
-    stream = _on(stream, k_pool, v_pool, copies, status)
-    with _Device(k_pool):
-        _check(load_library().gqa_pages_copy(
-            _ptr(k_pool), _ptr(v_pool), _ptr(copies), copies.shape[0], page_size, n_pages, H_kv, d,
-            dtype, _ptr(status), _stream(stream)))
+    n = copies.shape[0]
+    _want(v_pool, k_pool.shape, k_pool.dtype, "v_pool")
+    _want(copies, (n, 2), torch.int32, "copies")
+    dev = _tensors(k_pool, v_pool, copies, status)
+    _run(dev, lib.gqa_pages_copy, k_pool.data_ptr(), v_pool.data_ptr(), copies.data_ptr(), n, page_size, n_pages, H_kv, d, code,
+         _addr(status), _raw_stream(stream, dev))
