@@ -565,12 +565,20 @@ extern "C" int gqa_decode_paged_fp8(const void *q, const void *k_pool, const voi
 
 namespace {
 
+constexpr int kFewRows = 16;  // query rows of a unit of span_few.cu
+
 // What the span calls share: sizes that follow from the arguments, and the workspace's sections
 // (byte offsets).
 struct SpanPlan {
     int r, rb, HB, tb, blk, nblkQ, T, RT, unit_rows;
     long long u1, units, slot_floats;
     size_t uinfo, slots, res, res_ml, bytes;
+    // The launch for few query rows a span (span_few.cu): the own rows of sequences with few of
+    // them, or all of a cross attention of few tokens per sequence.
+    bool few = false;
+    int few_rb, few_workers;
+    long long few_u1;
+    size_t few_rec, few_uinfo, few_slots;
 };
 
 // P shared spans over N tokens, and own spans of B sequences (none: B = 0) of Q tokens.
@@ -586,8 +594,8 @@ bool span_plan(SpanPlan &s, int P, int N, int B, int Q, int H_q, int H_kv, int d
     s.unit_rows = tc ? 2 * s.RT : s.RT;
     s.nblkQ = (Q + s.blk - 1) / s.blk;
     const long long heads = static_cast<long long>(H_kv) * s.HB;
-    s.u1 = (static_cast<long long>(N) / s.blk + P + 1) * heads;
-    s.units = s.u1 + static_cast<long long>(B) * s.nblkQ * heads;
+    s.u1 = static_cast<long long>(N) / s.blk + P + 1;
+    s.units = (s.u1 + static_cast<long long>(B) * s.nblkQ) * heads;
     if (heads > 65535 || s.units > (1ll << 30) || static_cast<long long>(N) * H_q > (1ll << 30)) return false;
     s.slot_floats = static_cast<long long>(s.unit_rows) * (d + 2);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -597,6 +605,23 @@ bool span_plan(SpanPlan &s, int P, int N, int B, int Q, int H_q, int H_kv, int d
     const size_t rows = B > 0 ? 2ull * N * H_q : 0;
     s.res_ml = s.res + up(rows * d * 4);
     s.bytes = s.res_ml + up(rows * 8);
+    // With few query rows per span -- up to 16, on average over the encoder sequences -- a product
+    // of 128 of them is mostly padding and its chain of waits what is paid for.
+    const long long few_tokens = B > 0 ? Q : (static_cast<long long>(N) + P - 1) / P;
+    s.few = tc && few_tokens * s.r <= kFewRows;
+    if (s.few) {
+        s.few_rb = s.r;
+        s.few_workers = sms * span_few_warps(d);
+        const int blk = kFewRows / s.r;
+        s.few_u1 = static_cast<long long>(N) / blk + P + 1;
+        const size_t at = B > 0 ? s.bytes : 0;
+        const long long units = (B > 0 ? static_cast<long long>(B) * ((Q + blk - 1) / blk) : s.few_u1) * H_kv;
+        if (units > (1ll << 30)) return false;
+        s.few_rec = at;
+        s.few_uinfo = s.few_rec + up(static_cast<size_t>(s.few_workers) * sizeof(SpanRecord));
+        s.few_slots = s.few_uinfo + up(B > 0 ? units * sizeof(int4) : 0);
+        s.bytes = s.few_slots + up(2ull * s.few_workers * kFewRows * (d + 2) * 4);
+    }
     return true;
 }
 
@@ -670,7 +695,7 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
     p.status = status;
     // One CTA per SM, but no more than there can be tiles.
     const long long tiles_g = (static_cast<long long>(a.g_max) + s.T - 1) / s.T, tiles_o = (static_cast<long long>(a.own_max) + s.T - 1) / s.T;
-    const long long most = s.u1 * tiles_g + (s.units - s.u1) * tiles_o;
+    const long long most = s.units * (tiles_g > tiles_o ? tiles_g : tiles_o);
     p.G = most < sms ? static_cast<int>(most) : sms;
     const double scale_log2 = static_cast<double>(scale) * 1.4426950408889634;
     p.scale_log2 = static_cast<float>(scale_log2);
@@ -682,6 +707,8 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
         p.scale_log2 = static_cast<float>(std::fabs(scale_log2));
         if (p.scale_log2 < 1e-37f) p.scale_log2 = 1e-37f;
     }
+    p.s_begin = 0;
+    p.s_end = a.P + a.B;
     auto *w = static_cast<unsigned char *>(workspace);
     p.rec = reinterpret_cast<SpanRecord *>(w);
     p.uinfo = reinterpret_cast<int4 *>(w + s.uinfo);
@@ -690,39 +717,59 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
     p.res = reinterpret_cast<float *>(w + s.res);
     p.res_ml = reinterpret_cast<float *>(w + s.res_ml);
 
-    int res;
-    if (tc) {
-        if (encode_fn() == nullptr) return GQA_ERR_CUDA;
-        SpanMaps m;
-        // caches as (d, H_kv, rows, prefixes or sequences) or (d, H_kv, page_size, n_pages)
-        const int box = paged && a.page_size < s.T ? a.page_size : s.T;
-        const int rows_g = paged ? a.page_size : a.g_max, rows_o = paged ? a.page_size : a.own_max;
-        const int outer_g = paged ? a.n_pages : a.P, outer_o = paged ? a.n_pages : a.B;
-        if (!encode_q_map(&m.q_shared, a.q, a.N, s.tb, a.H_q, a.d, s.rb) ||
-            !encode_cache_map(&m.k_shared, a.k_shared, outer_g, a.H_kv, a.d, rows_g, box) ||
-            !encode_cache_map(&m.k_shared8, a.k_shared, outer_g, a.H_kv, a.d, rows_g, 8) ||
-            !encode_cache_map(&m.v_shared, a.v_shared, outer_g, a.H_kv, a.d, rows_g, box) ||
-            !encode_cache_map(&m.v_shared8, a.v_shared, outer_g, a.H_kv, a.d, rows_g, 8))
-            return GQA_ERR_SHAPE;
-        m.q_own = m.q_shared;
-        m.k_own = m.k_shared;
-        m.k_own8 = m.k_shared8;
-        m.v_own = m.v_shared;
-        m.v_own8 = m.v_shared8;
-        if (a.B > 0 && !encode_q_map(&m.q_own, a.q, a.N, a.Q < s.tb ? a.Q : s.tb, a.H_q, a.d, s.rb)) return GQA_ERR_SHAPE;
-        if (a.B > 0 && !paged &&
-            (!encode_cache_map(&m.k_own, a.k_own, outer_o, a.H_kv, a.d, rows_o, box) ||
-             !encode_cache_map(&m.k_own8, a.k_own, outer_o, a.H_kv, a.d, rows_o, 8) ||
-             !encode_cache_map(&m.v_own, a.v_own, outer_o, a.H_kv, a.d, rows_o, box) ||
-             !encode_cache_map(&m.v_own8, a.v_own, outer_o, a.H_kv, a.d, rows_o, 8)))
-            return GQA_ERR_SHAPE;
-        res = launch_span_tc(m, p, stream);
-    } else {
-        res = launch_span_f32(p, static_cast<const float *>(a.q), static_cast<const float *>(a.k_shared),
-                              static_cast<const float *>(a.v_shared), static_cast<const float *>(a.k_own),
-                              static_cast<const float *>(a.v_own), stream);
+    if (!tc) {
+        const int res = launch_span_f32(p, static_cast<const float *>(a.q), static_cast<const float *>(a.k_shared),
+                                        static_cast<const float *>(a.v_shared), static_cast<const float *>(a.k_own),
+                                        static_cast<const float *>(a.v_own), stream);
+        return res != GQA_OK ? res : launch_span_merge(p, p, stream);
     }
-    return res != GQA_OK ? res : launch_span_merge(p, stream);
+    SpanParams fp = p;
+    if (s.few) {
+        fp.rb = s.few_rb;
+        fp.HB = 1;
+        fp.tb = fp.blk = kFewRows / s.few_rb;
+        fp.nblkQ = (a.Q + fp.blk - 1) / fp.blk;
+        fp.T = fp.RT = fp.unit_rows = kFewRows;
+        fp.G = s.few_workers;
+        fp.u1 = 0;
+        fp.rec = reinterpret_cast<SpanRecord *>(w + s.few_rec);
+        fp.uinfo = reinterpret_cast<int4 *>(w + s.few_uinfo);
+        fp.slots = reinterpret_cast<float *>(w + s.few_slots);
+        fp.slot_floats = kFewRows * (a.d + 2);
+        if (a.B == 0) {
+            const int rc2 = launch_span_few(fp, a.q, a.k_shared, a.v_shared, stream);
+            return rc2 != GQA_OK ? rc2 : launch_span_merge(fp, fp, stream);
+        }
+        p.s_end = fp.s_begin = a.P;
+    }
+    if (encode_fn() == nullptr) return GQA_ERR_CUDA;
+    // caches as (d, H_kv, rows, prefixes or sequences) or (d, H_kv, page_size, n_pages)
+    const int rows_g = paged ? a.page_size : a.g_max, rows_o = paged ? a.page_size : a.own_max;
+    const int outer_g = paged ? a.n_pages : a.P, outer_o = paged ? a.n_pages : a.B;
+    const int box = paged && a.page_size < s.T ? a.page_size : s.T;
+    SpanMaps m;
+    if (!encode_q_map(&m.q_shared, a.q, a.N, s.tb, a.H_q, a.d, s.rb) ||
+        !encode_cache_map(&m.k_shared, a.k_shared, outer_g, a.H_kv, a.d, rows_g, box) ||
+        !encode_cache_map(&m.k_shared8, a.k_shared, outer_g, a.H_kv, a.d, rows_g, 8) ||
+        !encode_cache_map(&m.v_shared, a.v_shared, outer_g, a.H_kv, a.d, rows_g, box) ||
+        !encode_cache_map(&m.v_shared8, a.v_shared, outer_g, a.H_kv, a.d, rows_g, 8))
+        return GQA_ERR_SHAPE;
+    m.q_own = m.q_shared;
+    m.k_own = m.k_shared;
+    m.k_own8 = m.k_shared8;
+    m.v_own = m.v_shared;
+    m.v_own8 = m.v_shared8;
+    const bool own_here = a.B > 0 && !s.few;
+    if (own_here && !encode_q_map(&m.q_own, a.q, a.N, a.Q < s.tb ? a.Q : s.tb, a.H_q, a.d, s.rb)) return GQA_ERR_SHAPE;
+    if (own_here && !paged &&
+        (!encode_cache_map(&m.k_own, a.k_own, outer_o, a.H_kv, a.d, rows_o, box) ||
+         !encode_cache_map(&m.k_own8, a.k_own, outer_o, a.H_kv, a.d, rows_o, 8) ||
+         !encode_cache_map(&m.v_own, a.v_own, outer_o, a.H_kv, a.d, rows_o, box) ||
+         !encode_cache_map(&m.v_own8, a.v_own, outer_o, a.H_kv, a.d, rows_o, 8)))
+        return GQA_ERR_SHAPE;
+    int res = launch_span_tc(m, p, stream);
+    if (res == GQA_OK && s.few) res = launch_span_few(fp, a.q, a.k_own, a.v_own, stream);
+    return res != GQA_OK ? res : launch_span_merge(p, fp, stream);
 }
 
 }  // namespace

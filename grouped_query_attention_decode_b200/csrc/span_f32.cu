@@ -48,9 +48,9 @@ span_f32_kernel(const float *__restrict__ q, const float *__restrict__ ks, const
     SpanWalker w;
     w.init(p, cr);
     SpanSegment g;
-    if (tid == 0) open_notes(p, cr);
+    if (tid == 0) open_notes(p, cr, blockIdx.x);
     while (w.next(p, g)) {
-        if (tid == 0) note_unit(p, g, cr);
+        if (tid == 0) note_unit(p, g, cr, blockIdx.x);
         const bool shared = g.s < p.P;
         const float *const kc = shared ? ks : ko, *const vc = shared ? vs : vo;
         for (int i = tid; i < C::RT * (D / 4); i += 256) {

@@ -86,59 +86,58 @@ __device__ __forceinline__ int slot_row(const SpanParams &p, int tl, int hp) {
     return tile * p.RT + (tl - tile * p.tb) * p.rb + hp;
 }
 
-// Shared and own rows: one block per (token, key/value head, head block), a warp per query head.
+// Shared and own rows: one block per (token, key/value head), a warp per query head.  p[0] is the
+// launch over the shared spans, p[1] the one over the own ones.
 template <int V>
-__global__ void __launch_bounds__(256) span_merge_shared_kernel(const __grid_constant__ SpanParams p) {
+__global__ void __launch_bounds__(256) span_merge_shared_kernel(const __grid_constant__ SpanParams p0, const __grid_constant__ SpanParams p1) {
     grid_dependency_wait();
-    const int tok = blockIdx.x, kh = blockIdx.y, kvh = kh / p.HB, hb = kh - kvh * p.HB;
-    const int b = tok / p.Q;
-    const int lane = threadIdx.x & 31;
-    // the token's unit in its group's span and in its own, with the pieces of each
-    __shared__ int4 info[2];
-    __shared__ int tl_s[2], tiles_s[2], valid_s;
-    __shared__ long long total_s;
+    const int tok = blockIdx.x, kvh = blockIdx.y;
+    const int b = tok / p0.Q, lane = threadIdx.x & 31;
+    // the token's spans, found by two warps at once
+    __shared__ Span span_s[2];
+    __shared__ int valid_s[2];
+    __shared__ long long total_s[2];
     if (threadIdx.x == 0) {
-        int row0, rows, g = group_of(p, b);
-        bool valid = own_rows_of(p, b, row0, rows);
-        tiles_s[0] = 0;
+        const int g = group_of(p0, b);
+        Span sp = {0, 0, 0, 0, 0};
+        valid_s[0] = 1;
         if (g >= 0) {
-            const Span sp = span_at(p, g, false);
-            const int n = shared_rows_of(p, g);
-            valid = valid && n >= 0;
-            if (tok >= sp.tok0 && tok < sp.tok0 + sp.ntok && n > 0) {
-                const int block = (tok - sp.tok0) / p.blk;
-                tiles_s[0] = tiles_of(n, p.T);
-                tl_s[0] = tok - sp.tok0 - block * p.blk;
-                info[0] = unit_pieces_of(p, unit_number(p, g, sp.tok0, block, kvh, hb));
-            }
+            sp = span_at(p0, g, false);
+            if (tok < sp.tok0 || tok >= sp.tok0 + sp.ntok) sp.rows = 0;  // a group whose start is out of range
+            valid_s[0] = shared_rows_of(p0, g) >= 0;
         }
-        const int j = tok - b * p.Q, block = j / p.blk;
-        tiles_s[1] = tiles_of(rows, p.T);
-        tl_s[1] = j - block * p.blk;
-        if (rows > 0) info[1] = unit_pieces_of(p, unit_number(p, p.P + b, 0, block, kvh, hb));
-        valid_s = valid;
-        total_s = __ldcg(&p.rec->total);
+        sp.src = g;
+        span_s[0] = sp;
+        total_s[0] = __ldcg(&p0.rec->total);
+    } else if (threadIdx.x == 32) {
+        Span sp = {b * p0.Q, p0.Q, 0, 0, p0.P + b};
+        valid_s[1] = own_rows_of(p1, b, sp.row0, sp.rows);
+        span_s[1] = sp;
+        total_s[1] = __ldcg(&p1.rec->total);
     }
     __syncthreads();
-    const int heads = min(p.rb, p.r - hb * p.rb);
-    for (int hp = threadIdx.x >> 5; hp < heads; hp += 8) {
-        const long long row = static_cast<long long>(tok) * p.H_q + kvh * p.r + hb * p.rb + hp;
+    const bool valid = valid_s[0] && valid_s[1];
+    for (int h = threadIdx.x >> 5; h < p0.r; h += 8) {
+        const long long row = static_cast<long long>(tok) * p0.H_q + kvh * p0.r + h;
         Join<V> j;
-        if (valid_s) {
+        if (valid) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                if (tiles_s[c] == 0) continue;
-                const int4 u = info[c];
+                const SpanParams &p = c == 0 ? p0 : p1;
+                const Span sp = span_s[c];
+                if (sp.rows == 0) continue;
+                const int hb = h / p.rb, tl = tok - sp.tok0, block = tl / p.blk;
+                const int4 u = unit_pieces_of(p, unit_number(p, sp.src, sp, block, kvh, hb));
                 if (u.x == u.z) {
                     const long long rr = (c == 0 ? 0 : static_cast<long long>(p.N) * p.H_q) + row;
                     const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.res_ml) + rr);
                     j.add(ml.x, ml.y, __ldcg(reinterpret_cast<const typename Vec<V>::type *>(p.res + rr * p.d) + lane));
                 } else {
-                    add_pieces<V>(p, total_s, u.x, u.y, u.z, slot_row(p, tl_s[c], hp), lane, j);
+                    add_pieces<V>(p, total_s[c], u.x, u.y, u.z, slot_row(p, tl - block * p.blk, h - hb * p.rb), lane, j);
                 }
             }
         }
-        j.store(p.out + row * p.d + lane * V);
+        j.store(p0.out + row * p0.d + lane * V);
     }
 }
 
@@ -167,8 +166,8 @@ __global__ void __launch_bounds__(256) span_merge_cross_kernel(const __grid_cons
     }
 }
 
-template <class K>
-int launch(K kern, dim3 grid, const SpanParams &p, cudaStream_t stream) {
+template <class... K, class... A>
+int launch(void (*kern)(K...), dim3 grid, cudaStream_t stream, const A &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(256);
@@ -178,18 +177,20 @@ int launch(K kern, dim3 grid, const SpanParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 }  // namespace
 
-int launch_span_merge(const SpanParams &p, cudaStream_t stream) {
-    if (p.B > 0) {
-        const dim3 grid(p.N, p.H_kv * p.HB);
-        return p.d == 128 ? launch(span_merge_shared_kernel<4>, grid, p, stream) : launch(span_merge_shared_kernel<2>, grid, p, stream);
+int launch_span_merge(const SpanParams &shared, const SpanParams &own, cudaStream_t stream) {
+    const SpanParams &p = shared;
+    if (own.B > 0) {
+        const dim3 grid(p.N, p.H_kv);
+        return p.d == 128 ? launch(span_merge_shared_kernel<4>, grid, stream, p, own) : launch(span_merge_shared_kernel<2>, grid, stream, p, own);
     }
-    const dim3 grid(p.G, 4);
-    return p.d == 128 ? launch(span_merge_cross_kernel<4>, grid, p, stream) : launch(span_merge_cross_kernel<2>, grid, p, stream);
+    // A cut unit's rows: with few of them a warp or two each, with 256 enough warps that each has one or two.
+    const dim3 grid(p.G, p.unit_rows <= 16 ? 1 : p.unit_rows / 16);
+    return p.d == 128 ? launch(span_merge_cross_kernel<4>, grid, stream, p) : launch(span_merge_cross_kernel<2>, grid, stream, p);
 }
 
 }  // namespace gqa

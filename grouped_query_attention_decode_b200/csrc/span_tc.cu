@@ -664,7 +664,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
         // ------------------------------------------------------------------ planner
         if (lane == 0) {
             const SpanRange cr = sm->range;
-            open_notes(p, cr);
+            open_notes(p, cr, blockIdx.x);
             SpanWalker w;
             w.init(p, cr);
             SpanPiece piece;
@@ -673,7 +673,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 more = w.next(p, piece.g);
                 piece.pair = piece.last_rows = piece.steps = 0;
                 if (more) {
-                    note_unit(p, piece.g, cr);
+                    note_unit(p, piece.g, cr, blockIdx.x);
                     piece.pair = piece.g.ntok > p.tb;
                     piece.steps = piece.pair ? 2 * piece.g.len : piece.g.len;
                     piece.last_rows = min(T, piece.g.rows - (piece.g.j0 + piece.g.len - 1) * T);

@@ -30,6 +30,7 @@ struct SpanParams {
     // own_after (paged), the rows [glen[its group], lens[b]) of its block table
     const int32_t *lens;
     int B, own_max, own_after;
+    int s_begin, s_end;  // spans that take part: [0, P) are the shared ones, [P, P + B) the own ones
     int Q, N;  // tokens per member (1 for cross attention), tokens in all
     int H_q, H_kv, d, r;
     int rb, HB, tb;  // heads per row tile, head blocks = ceil(r / rb), tokens per row tile
@@ -50,7 +51,7 @@ struct SpanParams {
     float *slots;          // [2 * G][slot_floats]
     long long slot_floats;
     float *res, *res_ml;   // [2][N * H_q][d] sums and [2][N * H_q][2] (m, l) of whole units
-    int u1;                // first unit number of the own spans
+    int u1;                // number of the own spans' first token block, after the shared spans'
     int unit_rows;         // query rows of a slot
 };
 
@@ -129,11 +130,12 @@ __device__ __forceinline__ long long span_tiles(const SpanParams &p, const Span 
     return static_cast<long long>(tiles_of(sp.rows, p.T)) * span_blocks(p, sp) * p.H_kv * p.HB;
 }
 
-// Unit number of block `block` of span s.  Shared spans: blocks are numbered by their first
-// token / blk + group, which grows along the line, so no two blocks share a number.
-__device__ __forceinline__ int unit_number(const SpanParams &p, int s, int tok0, int block, int kvh, int hb) {
-    const int k = s < p.P ? tok0 / p.blk + block + s : (s - p.P) * p.nblkQ + block;
-    return (s < p.P ? 0 : p.u1) + (k * p.H_kv + kvh) * p.HB + hb;
+// Number of a span's unit `block` of key/value head kvh and head block hb.  Token blocks of shared
+// spans are numbered by their first token / blk + group: that grows along the line by at least the
+// span's blocks, so no two share a number, and unit numbers grow along the line.
+__device__ __forceinline__ int unit_number(const SpanParams &p, int s, const Span &sp, int block, int kvh, int hb) {
+    const int base = s < p.P ? sp.tok0 / p.blk + s : p.u1 + (s - p.P) * p.nblkQ;
+    return base * p.H_kv * p.HB + (kvh * p.HB + hb) * span_blocks(p, sp) + block;
 }
 
 struct SpanRange {
@@ -146,8 +148,8 @@ struct SpanRange {
 template <int NT>
 __device__ void locate_span_range(const SpanParams &p, int cta, long long *scratch, SpanRange *res) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int spans = p.P + p.B, per = (spans + NT - 1) / NT;
-    const int s0 = tid * per, s1 = min(spans, s0 + per);
+    const int per = (p.s_end - p.s_begin + NT - 1) / NT;
+    const int s0 = p.s_begin + tid * per, s1 = min(p.s_end, s0 + per);
     long long mine = 0;
     for (int s = s0; s < s1; ++s) mine += span_tiles(p, span_at(p, s, cta == 0));
     const long long incl = warp_incl_scan(mine, lane);
@@ -178,6 +180,34 @@ __device__ void locate_span_range(const SpanParams &p, int cta, long long *scrat
         }
     }
     __syncthreads();
+}
+
+// The same by one warp, for worker `cta`.
+__device__ inline SpanRange locate_span_range_warp(const SpanParams &p, int cta, int lane) {
+    SpanRange r = {0, 0, 0, 0, 0};
+    for (int s0 = p.s_begin; s0 < p.s_end; s0 += 32) {
+        const int s = s0 + lane;
+        const long long v = s < p.s_end ? span_tiles(p, span_at(p, s, cta == 0)) : 0;
+        r.total += __shfl_sync(kFullMask, warp_incl_scan(v, lane), 31);
+    }
+    r.begin = cta_range_begin(cta, r.total, p.G);
+    r.end = cta_range_begin(cta + 1, r.total, p.G);
+    if (r.begin >= r.end) return r;
+    long long off = 0;
+    for (int s0 = p.s_begin; s0 < p.s_end; s0 += 32) {
+        const int s = s0 + lane;
+        const long long v = s < p.s_end ? span_tiles(p, span_at(p, s, false)) : 0;
+        const long long incl = warp_incl_scan(v, lane);
+        const uint32_t m = __ballot_sync(kFullMask, off + incl - v <= r.begin && r.begin < off + incl);
+        if (m != 0) {
+            const int l = __ffs(m) - 1;
+            r.s0 = s0 + l;
+            r.off0 = off + __shfl_sync(kFullMask, incl - v, l);
+            return r;
+        }
+        off += __shfl_sync(kFullMask, incl, 31);
+    }
+    return r;  // unreachable when begin < total
 }
 
 // One CTA-range piece of one unit.
@@ -218,7 +248,7 @@ struct SpanWalker {
         const int hv = p.H_kv * p.HB;
         while (t >= off + static_cast<long long>(nt) * nblk * hv) {
             off += static_cast<long long>(nt) * nblk * hv;
-            if (++s >= p.P + p.B) {  // cannot happen while t < total
+            if (++s >= p.s_end) {  // cannot happen while t < total
                 t = end;
                 return false;
             }
@@ -239,7 +269,7 @@ struct SpanWalker {
         const long long left = end - t;
         g.len = static_cast<int>(left < nt - g.j0 ? left : nt - g.j0);
         g.nt = nt;
-        g.unit = unit_number(p, s, sp.tok0, block, g.kvh, g.hb);
+        g.unit = unit_number(p, s, sp, block, g.kvh, g.hb);
         g.uoff = off + static_cast<long long>(k) * nt;
         g.first = !opened;
         opened = true;
@@ -263,18 +293,17 @@ __device__ __forceinline__ int seen_rows(const SpanParams &p, const SpanSegment 
     return g.s < p.P || p.Q == 1 ? g.rows : g.rows - p.Q + 1 + token % p.Q;
 }
 
-// One thread of a CTA, before its segments.
-__device__ __forceinline__ void open_notes(const SpanParams &p, const SpanRange &cr) {
-    if (p.B == 0) p.rec[blockIdx.x].valid = 0;
-    else if (blockIdx.x == 0) p.rec[0].total = cr.total;
+// One thread of worker `cta` (a CTA, or a warp of span_few.cu), before its segments.
+__device__ __forceinline__ void open_notes(const SpanParams &p, const SpanRange &cr, int cta) {
+    if (p.B == 0) p.rec[cta].valid = 0;
+    else if (cta == 0) p.rec[0].total = cr.total;
 }
 
 // The same thread, once per segment: what the merge needs to find the unit's pieces.
-__device__ inline void note_unit(const SpanParams &p, const SpanSegment &g, const SpanRange &cr) {
+__device__ inline void note_unit(const SpanParams &p, const SpanSegment &g, const SpanRange &cr, int c0) {
     if (g.j0 != 0) return;
-    const int c0 = blockIdx.x;
     const int c1 = g.whole() ? c0 : static_cast<int>(cta_of_tile(g.uoff + g.nt - 1, cr.total, p.G));
-    if (p.B > 0) {
+    if (p.B > 0) {  // there are own rows to join with, here or in another launch
         p.uinfo[g.unit] = make_int4(c0, g.first ? 0 : 1, c1, 0);
     } else if (!g.whole()) {
         p.rec[c0] = SpanRecord{cr.total, 1, g.tok0, g.ntok, g.kvh, g.hb, g.first ? 0 : 1, c1, 0};
@@ -293,6 +322,11 @@ struct SpanMaps {
 int launch_span_tc(const SpanMaps &maps, const SpanParams &p, cudaStream_t stream);
 int launch_span_f32(const SpanParams &p, const float *q, const float *ks, const float *vs, const float *ko,
                     const float *vo, cudaStream_t stream);
-int launch_span_merge(const SpanParams &p, cudaStream_t stream);
+// Joins the pieces of one launch over the shared spans and one over the own ones (the same launch,
+// or none: own.B = 0).
+int launch_span_merge(const SpanParams &shared, const SpanParams &own, cudaStream_t stream);
+// The kernel for few query rows per span; p.G is the number of warps (span_few_warps a CTA).
+int launch_span_few(const SpanParams &p, const void *q, const void *k, const void *v, cudaStream_t stream);
+int span_few_warps(int d);
 
 }  // namespace gqa

@@ -120,3 +120,35 @@ def test_far_rows():
     bound = tolerance(q, [k[-1, -200:]], [v[-1, -200:]], 0.3, S)
     for i in range(3):
         assert float((out[i].double() - attend64(q[i], k[-1], v[-1], 0.3)).abs().max()) <= bound
+
+
+@pytest.mark.parametrize("heads", [(8, 8, 64), (8, 2, 64), (64, 2, 128), (12, 4, 128), (24, 1, 64)], ids=lambda h: "%d_%d_%d" % h)
+@pytest.mark.parametrize("tokens", [[1, 1, 1], [2, 0, 1, 3], [1, 0, 0, 0, 0, 0, 0, 40], [4] * 9], ids=str)
+def test_few_tokens(tokens, heads):
+    """One token, a beam or two per encoder sequence, and one sequence with many more than the mean."""
+    states = [(i * 211) % 700 for i in range(len(tokens))]  # the first has none
+    x = make(tokens, states, heads, torch.bfloat16, before=1, behind=2)
+    out, status = run(x, 0.1, out=torch.full(x["q"].shape, 7.0, device="cuda"))
+    assert status == 0
+    check(x, out, 0.1)
+    assert (out[0] == 7).all() and (out[-2:] == 7).all()
+
+
+def test_few_tokens_out_of_range():
+    x = make([1, 1, 1], [100, 90, 80], (8, 8, 64), torch.bfloat16)
+    good, _ = run(x, 0.1)
+    out, status = run(dict(x, states=[100, -1, 80]), 0.1)
+    assert status == gqa.STATUS_SEQLEN_RANGE and torch.equal(out[::2], good[::2]) and not out[1].any()
+    out, status = run(dict(x, starts=[0, 1, 0, 3]), 0.1)
+    # sequence 2 is now [0, 3), so token 0 is no longer sequence 0's alone
+    assert status == gqa.STATUS_GROUP_RANGE
+
+
+def test_few_tokens_repeat():
+    # the workspace's counters are set anew by each call
+    x = make([1] * 5, [700, 3, 2000, 129, 0], (16, 4, 128), torch.bfloat16)
+    ws = torch.full((gqa.cross_workspace_size(5, 5, 16, 4, 128, torch.bfloat16),), 255, dtype=torch.uint8, device="cuda")
+    first, _ = run(x, 0.1, workspace=ws)
+    again, _ = run(x, 0.1, workspace=ws)
+    assert torch.equal(first, again)
+    check(x, first, 0.1)
