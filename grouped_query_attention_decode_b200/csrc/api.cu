@@ -741,6 +741,7 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
             return rc2 != GQA_OK ? rc2 : launch_span_merge(fp, fp, stream);
         }
         p.s_end = fp.s_begin = a.P;
+        fp.behind_shared = 1;
     }
     if (encode_fn() == nullptr) return GQA_ERR_CUDA;
     // caches as (d, H_kv, rows, prefixes or sequences) or (d, H_kv, page_size, n_pages)

@@ -48,7 +48,7 @@ span_f32_kernel(const float *__restrict__ q, const float *__restrict__ ks, const
     SpanWalker w;
     w.init(p, cr);
     SpanSegment g;
-    if (tid == 0) open_notes(p, cr, blockIdx.x);
+    if (tid == 0) open_notes(p, blockIdx.x);
     while (w.next(p, g)) {
         if (tid == 0) note_unit(p, g, cr, blockIdx.x);
         const bool shared = g.s < p.P;

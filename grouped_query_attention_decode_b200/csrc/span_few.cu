@@ -75,11 +75,16 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
     const int worker = blockIdx.x * C::WARPS + (threadIdx.x >> 5);
     const uint32_t ring = smem_u32(few_smem) + (threadIdx.x >> 5) * (S * 2 * C::TILE);
 
-    grid_dependency_wait();
+    // Behind the launch over the shared rows nothing here depends on it: what that launch waited for
+    // before it let this one start is all that is read.  The launch behind this one has to find both
+    // complete, so the wait comes at the end.
+    if (!p.behind_shared) grid_dependency_wait();
     grid_launch_dependents();
-    if (worker >= p.G) return;
-    const SpanRange cr = locate_span_range_warp(p, worker, lane);
-    if (lane == 0) open_notes(p, cr, worker);
+    // in the ring, which nothing uses yet
+    auto *const before = reinterpret_cast<long long *>(few_smem);
+    const SpanRange cr = locate_warp_ranges<C::WARPS * 32>(p, worker, blockIdx.x == 0, before, before + C::WARPS * 32);
+    __syncthreads();
+    if (lane == 0) open_notes(p, worker);
 
     // The copies run S - 1 tiles ahead, with a walker of their own.
     SpanWalker cw;
@@ -88,23 +93,33 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
     int cj = 0;
     bool copies_left = cw.next(p, cg);
     int n_copied = 0;
+    // 16-row tiles start on multiples of 8 rows of the table, so a tile has at most two pages.  Their
+    // numbers are read when the copy before is issued.
+    int pages[2];
+    auto look_up = [&]() {
+        if constexpr (PAGED) {
+            const int t0 = (cg.j0 + cj) * T;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                pages[h] = copies_left && t0 + 8 * h < cg.rows
+                               ? __ldg(p.block_table + static_cast<long long>(cg.src) * p.max_pages + (cg.row0 + t0 + 8 * h) / p.page_size)
+                               : 0;
+        }
+    };
+    look_up();
     auto copy_tile = [&]() {
         if (copies_left) {
             const int t0 = (cg.j0 + cj) * T, rows = cg.rows - t0;  // rows left from here on
             const uint32_t dst = ring + (n_copied % S) * (2 * C::TILE);
-            // 16-row tiles start on multiples of 8 rows of the table, so a tile has at most two pages
             long long base[2];
             if constexpr (PAGED) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int row = cg.row0 + t0 + 8 * h;
-                    int pg = 0;
-                    if (8 * h < rows) {
-                        pg = __ldg(p.block_table + static_cast<long long>(cg.src) * p.max_pages + row / p.page_size);
-                        if (pg < 0 || pg >= p.n_pages) {
-                            if (p.status != nullptr) atomicOr(p.status, GQA_STATUS_PAGE_RANGE);
-                            pg = 0;
-                        }
+                    int pg = pages[h];
+                    if (pg < 0 || pg >= p.n_pages) {
+                        if (p.status != nullptr) atomicOr(p.status, GQA_STATUS_PAGE_RANGE);
+                        pg = 0;
                     }
                     base[h] = static_cast<long long>(pg) * p.page_size + row % p.page_size - 8 * h;
                 }
@@ -128,6 +143,7 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
                 copies_left = cw.next(p, cg);
                 cj = 0;
             }
+            look_up();
         }
         copy_commit();  // an empty group keeps the count
     };
@@ -268,6 +284,7 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
                 *reinterpret_cast<float2 *>(dst + 8 * j + 2 * (lane % 4)) = make_float2(o[j][2 * h] * norm, o[j][2 * h + 1] * norm);
         }
     }
+    if (p.behind_shared) grid_dependency_wait();
 }
 
 namespace {

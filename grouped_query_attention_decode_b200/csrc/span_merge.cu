@@ -1,8 +1,7 @@
 // Joins the pieces that the span kernels left in the workspace (spans.cuh): with pieces c of a
 // row's attended rows, each an unnormalised sum o_c, its reference m_c and l_c,
 //     M = max_c m_c,  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
-// One warp per query row, d / 32 columns a lane.  It is launched with the programmatic
-// attribute, so its blocks are resident when the span kernel's last CTA ends.
+// Eight lanes per query row.
 #include <cstdint>
 
 #include "device.cuh"
@@ -13,60 +12,60 @@ namespace gqa {
 
 namespace {
 
-template <int V>
-struct Vec;
-template <>
-struct Vec<2> { using type = float2; };
-template <>
-struct Vec<4> { using type = float4; };
-
-// A row's running join; V columns a lane.
-template <int V>
+// A row's running join, eight lanes a row: lane `sub` holds the columns 32 k + 4 sub .. + 3.
+template <int D>
 struct Join {
-    float M = -INFINITY, L = 0.f, o[V] = {};
+    static constexpr int NV = D / 32;
+    float M = -INFINITY, L = 0.f;
+    float4 o[NV] = {};
 
-    __device__ void add(float m, float l, typename Vec<V>::type ov) {
-        if (m == -INFINITY) return;  // a piece in which the row saw nothing: its sum is not looked at
-        const float top = fmaxf(M, m);
-        const float a = M == -INFINITY ? 0.f : ex2_approx(M - top), b = ex2_approx(m - top);
-        const float *x = reinterpret_cast<const float *>(&ov);
+    __device__ __forceinline__ void add(float2 ml, const float4 (&x)[NV]) {
+        const float top = fmaxf(M, ml.x);
+        // a piece in which the row saw nothing weighs nothing, and its sum is not looked at
+        const float a = M == -INFINITY ? 0.f : ex2_approx(M - top), b = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
         M = top;
-        L = L * a + l * b;
+        L = L * a + ml.y * b;
 #pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = o[k] * a + x[k] * b;
+        for (int k = 0; k < NV; ++k) {
+            o[k].x = o[k].x * a + (b == 0.f ? 0.f : x[k].x * b);
+            o[k].y = o[k].y * a + (b == 0.f ? 0.f : x[k].y * b);
+            o[k].z = o[k].z * a + (b == 0.f ? 0.f : x[k].z * b);
+            o[k].w = o[k].w * a + (b == 0.f ? 0.f : x[k].w * b);
+        }
     }
-    __device__ void store(float *dst) const {
-        typename Vec<V>::type r;
-        float *x = reinterpret_cast<float *>(&r);
+    __device__ __forceinline__ void store(float *dst, int sub) const {
         const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // no rows at all: zeros
 #pragma unroll
-        for (int k = 0; k < V; ++k) x[k] = o[k] * inv;
-        *reinterpret_cast<typename Vec<V>::type *>(dst) = r;
+        for (int k = 0; k < NV; ++k)
+            *reinterpret_cast<float4 *>(dst + 32 * k + 4 * sub) = make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv);
     }
 };
 
-// Adds row `srow` of every piece of a unit cut at CTA boundaries c0 .. c1.  The CTAs between
-// hold one piece each, except that with fewer tiles than CTAs some hold none.
-template <int V>
-__device__ void add_pieces(const SpanParams &p, long long total, int c0, int k0, int c1, int srow, int lane, Join<V> &j) {
-    using T = typename Vec<V>::type;
-    constexpr int AT_ONCE = 8;  // pieces whose loads are in flight together
-    for (int c = c0; c <= c1; c += AT_ONCE) {
+// Adds row `srow` of the pieces c0 + part, c0 + part + parts, ... of a cut unit's c0 .. c1, two
+// pieces' reads in flight at a time.  (Short code: it runs once, and every 8 instructions are a
+// fetch.)
+template <int D>
+__device__ __forceinline__ void add_pieces(const SpanParams &p, int c0, int k0, int c1, int srow, int sub, int part, int parts,
+                                           Join<D> &j) {
+    constexpr int NV = D / 32, AT_ONCE = 2;
+    const int ml_at = p.unit_rows * D + 2 * srow, o_at = srow * D + 4 * sub;
+#pragma unroll 1
+    for (int c = c0 + part; c <= c1; c += AT_ONCE * parts) {
         float2 ml[AT_ONCE];
-        T o[AT_ONCE];
+        float4 x[AT_ONCE][NV];
 #pragma unroll
         for (int u = 0; u < AT_ONCE; ++u) {
-            const int cc = c + u;
-            ml[u] = make_float2(-INFINITY, 0.f);
-            if (cc <= c1 && (total >= p.G || cta_range_begin(cc, total, p.G) < cta_range_begin(cc + 1, total, p.G))) {
-                const float *slot = p.slots + (2ll * cc + (cc == c0 ? k0 : 0)) * p.slot_floats;
-                ml[u] = __ldcg(reinterpret_cast<const float2 *>(slot + p.unit_rows * p.d + 2 * srow));
-                o[u] = __ldcg(reinterpret_cast<const T *>(slot + static_cast<long long>(srow) * p.d) + lane);
+            const int cc = c + u * parts;
+            if (cc <= c1) {
+                const float *at = p.slots + (2ll * cc + (cc == c0 ? k0 : 0)) * p.slot_floats;
+                ml[u] = __ldcg(reinterpret_cast<const float2 *>(at + ml_at));
+#pragma unroll
+                for (int k = 0; k < NV; ++k) x[u][k] = __ldcg(reinterpret_cast<const float4 *>(at + o_at + 32 * k));
             }
         }
 #pragma unroll
         for (int u = 0; u < AT_ONCE; ++u)
-            if (c + u <= c1) j.add(ml[u].x, ml[u].y, o[u]);
+            if (c + u * parts <= c1) j.add(ml[u], x[u]);
     }
 }
 
@@ -86,83 +85,90 @@ __device__ __forceinline__ int slot_row(const SpanParams &p, int tl, int hp) {
     return tile * p.RT + (tl - tile * p.tb) * p.rb + hp;
 }
 
-// Shared and own rows: one block per (token, key/value head), a warp per query head.  p[0] is the
-// launch over the shared spans, p[1] the one over the own ones.
-template <int V>
-__global__ void __launch_bounds__(256) span_merge_shared_kernel(const __grid_constant__ SpanParams p0, const __grid_constant__ SpanParams p1) {
-    grid_dependency_wait();
-    const int tok = blockIdx.x, kvh = blockIdx.y;
-    const int b = tok / p0.Q, lane = threadIdx.x & 31;
-    // the token's spans, found by two warps at once
-    __shared__ Span span_s[2];
-    __shared__ int valid_s[2];
-    __shared__ long long total_s[2];
-    if (threadIdx.x == 0) {
-        const int g = group_of(p0, b);
-        Span sp = {0, 0, 0, 0, 0};
-        valid_s[0] = 1;
-        if (g >= 0) {
-            sp = span_at(p0, g, false);
-            if (tok < sp.tok0 || tok >= sp.tok0 + sp.ntok) sp.rows = 0;  // a group whose start is out of range
-            valid_s[0] = shared_rows_of(p0, g) >= 0;
-        }
-        sp.src = g;
-        span_s[0] = sp;
-        total_s[0] = __ldcg(&p0.rec->total);
-    } else if (threadIdx.x == 32) {
-        Span sp = {b * p0.Q, p0.Q, 0, 0, p0.P + b};
-        valid_s[1] = own_rows_of(p1, b, sp.row0, sp.rows);
-        span_s[1] = sp;
-        total_s[1] = __ldcg(&p1.rec->total);
-    }
-    __syncthreads();
-    const bool valid = valid_s[0] && valid_s[1];
-    for (int h = threadIdx.x >> 5; h < p0.r; h += 8) {
-        const long long row = static_cast<long long>(tok) * p0.H_q + kvh * p0.r + h;
-        Join<V> j;
-        if (valid) {
+// Row `row` (token tok, head h of its group) of span sp of a launch, added to the join.
+template <int D>
+__device__ __forceinline__ void add_span(const SpanParams &p, int s, const Span &sp, int tok, int kvh, int h, long long row, bool own,
+                                         int sub, int part, int parts, Join<D> &j) {
+    const int hb = h / p.rb, tl = tok - sp.tok0, block = tl / p.blk;
+    const int4 u = unit_pieces_of(p, unit_number(p, s, sp, block, kvh, hb));
+    if (u.x == u.z) {
+        if (part != 0) return;
+        const long long rr = (own ? static_cast<long long>(p.N) * p.H_q : 0) + row;
+        float4 x[D / 32];
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.res_ml) + rr);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const SpanParams &p = c == 0 ? p0 : p1;
-                const Span sp = span_s[c];
-                if (sp.rows == 0) continue;
-                const int hb = h / p.rb, tl = tok - sp.tok0, block = tl / p.blk;
-                const int4 u = unit_pieces_of(p, unit_number(p, sp.src, sp, block, kvh, hb));
-                if (u.x == u.z) {
-                    const long long rr = (c == 0 ? 0 : static_cast<long long>(p.N) * p.H_q) + row;
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.res_ml) + rr);
-                    j.add(ml.x, ml.y, __ldcg(reinterpret_cast<const typename Vec<V>::type *>(p.res + rr * p.d) + lane));
-                } else {
-                    add_pieces<V>(p, total_s[c], u.x, u.y, u.z, slot_row(p, tl - block * p.blk, h - hb * p.rb), lane, j);
-                }
-            }
-        }
-        j.store(p0.out + row * p0.d + lane * V);
+        for (int k = 0; k < D / 32; ++k) x[k] = __ldcg(reinterpret_cast<const float4 *>(p.res + rr * D + 32 * k + 4 * sub));
+        j.add(ml, x);
+    } else {
+        add_pieces<D>(p, u.x, u.y, u.z, slot_row(p, tl - block * p.blk, h - hb * p.rb), sub, part, parts, j);
     }
 }
 
-// Cross attention: block (c, part) joins a part of the rows of the cut unit that starts in CTA c,
-// and of the tokens whose encoder sequence has no states writes zeros.
-template <int V>
-__global__ void __launch_bounds__(256) span_merge_cross_kernel(const __grid_constant__ SpanParams p) {
+// Shared and own rows, eight lanes per (token, query head), or a warp, whose four groups of eight
+// share a unit's pieces (parts = 4).  p0 is the launch over the shared spans, p1 the one over the own ones.  What bounds it is the chain of reads -- group, lengths,
+// pieces of the unit, the pieces -- so nothing is looked up by one thread for others.
+template <int D>
+__global__ void __launch_bounds__(256, 3) span_merge_shared_kernel(const __grid_constant__ SpanParams p0, const __grid_constant__ SpanParams p1, int parts) {
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31, warp = blockIdx.y * 8 + (threadIdx.x >> 5), warps = gridDim.y * 8;
-    const SpanRecord u = p.rec[blockIdx.x];
-    if (u.valid) {
-        const int heads = min(p.rb, p.r - u.hb * p.rb);
-        for (int i = warp; i < u.ntok * heads; i += warps) {
-            const int tl = i / heads, hp = i - tl * heads;
-            Join<V> j;
-            add_pieces<V>(p, u.total, blockIdx.x, u.k0, u.c1, slot_row(p, tl, hp), lane, j);
-            j.store(p.out + (static_cast<long long>(u.tok0 + tl) * p.H_q + u.kvh * p.r + u.hb * p.rb + hp) * p.d + lane * V);
+    const int sub = threadIdx.x & 7, part = (threadIdx.x >> 3) & (parts - 1);
+    const long long row = (static_cast<long long>(blockIdx.x) * 32 + (threadIdx.x >> 3)) / parts;
+    if (row >= static_cast<long long>(p0.N) * p0.H_q) return;  // whole warps where parts = 4
+    const int tok = static_cast<int>(row / p0.H_q), head = static_cast<int>(row - static_cast<long long>(tok) * p0.H_q);
+    const int kvh = head / p0.r, h = head - kvh * p0.r;
+    const int b = tok / p0.Q;
+    const int n = __ldg(p1.lens + b);
+    const int g = group_of(p0, b);
+    Span sg = {0, 0, 0, 0, 0}, so = {b * p0.Q, p0.Q, 0, 0, 0};
+    bool valid = true;
+    if (g >= 0) {
+        sg = span_at(p0, g, false);
+        valid = shared_rows_of(p0, g) >= 0;
+        if (p1.own_after) so.row0 = max(sg.rows, 0);
+        if (tok < sg.tok0 || tok >= sg.tok0 + sg.ntok) sg.rows = 0;  // a group whose start is out of range
+    }
+    valid = valid && n >= so.row0 && n <= p1.own_max && (p1.Q == 1 || n - so.row0 >= p1.Q);  // own_rows_of
+    so.rows = n - so.row0;
+    Join<D> j;
+    if (valid && sg.rows > 0) add_span<D>(p0, g, sg, tok, kvh, h, row, false, sub, part, parts, j);
+    if (valid && so.rows > 0) add_span<D>(p1, p1.P + b, so, tok, kvh, h, row, true, sub, part, parts, j);
+    if (parts == 4) {
+#pragma unroll
+        for (int x = 8; x <= 16; x <<= 1) {
+            float4 o[D / 32];
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+                o[k] = make_float4(__shfl_xor_sync(kFullMask, j.o[k].x, x), __shfl_xor_sync(kFullMask, j.o[k].y, x),
+                                   __shfl_xor_sync(kFullMask, j.o[k].z, x), __shfl_xor_sync(kFullMask, j.o[k].w, x));
+            j.add(make_float2(__shfl_xor_sync(kFullMask, j.M, x), __shfl_xor_sync(kFullMask, j.L, x)), o);
+        }
+    }
+    if (part == 0) j.store(p0.out + row * D, sub);
+}
+
+// Cross attention: `slices` warps join the rows of the cut unit that starts in a worker, four at a
+// time, and the tokens whose encoder sequence has no states get zeros.
+template <int D>
+__global__ void __launch_bounds__(256, 3) span_merge_cross_kernel(const __grid_constant__ SpanParams p, int slices) {
+    grid_dependency_wait();
+    const int sub = threadIdx.x & 7, warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int worker = warp / slices, slice = warp - worker * slices;
+    if (worker < p.G) {
+        const SpanRecord u = p.rec[worker];
+        if (u.valid) {
+            const int heads = min(p.rb, p.r - u.hb * p.rb);
+            for (int i = 4 * slice + (threadIdx.x >> 3 & 3); i < u.ntok * heads; i += 4 * slices) {
+                const int tl = i / heads, hp = i - tl * heads;
+                Join<D> j;
+                add_pieces<D>(p, worker, u.k0, u.c1, slot_row(p, tl, hp), sub, 0, 1, j);
+                j.store(p.out + (static_cast<long long>(u.tok0 + tl) * p.H_q + u.kvh * p.r + u.hb * p.rb + hp) * D, sub);
+            }
         }
     }
     for (int e = blockIdx.x; e < p.P; e += gridDim.x) {
         const Span sp = span_at(p, e, false);
         if (sp.rows > 0) continue;
-        const long long n = static_cast<long long>(sp.ntok) * p.H_q * p.d / 4, at = static_cast<long long>(sp.tok0) * p.H_q * p.d / 4;
-        for (long long i = blockIdx.y * 256 + threadIdx.x; i < n; i += gridDim.y * 256)
-            reinterpret_cast<float4 *>(p.out)[at + i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const long long n = static_cast<long long>(sp.ntok) * p.H_q * D / 4, at = static_cast<long long>(sp.tok0) * p.H_q * D / 4;
+        for (long long i = threadIdx.x; i < n; i += 256) reinterpret_cast<float4 *>(p.out)[at + i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -185,12 +191,17 @@ int launch(void (*kern)(K...), dim3 grid, cudaStream_t stream, const A &...args)
 int launch_span_merge(const SpanParams &shared, const SpanParams &own, cudaStream_t stream) {
     const SpanParams &p = shared;
     if (own.B > 0) {
-        const dim3 grid(p.N, p.H_kv);
-        return p.d == 128 ? launch(span_merge_shared_kernel<4>, grid, stream, p, own) : launch(span_merge_shared_kernel<2>, grid, stream, p, own);
+        // With few rows the shared spans are cut into many pieces (19 for 16 sequences over 8
+        // key/value heads: 14 us by eight lanes a row, 9 by a warp) and there are SMs enough for a
+        // warp a row; 8192 rows of few pieces take 11 us by eight lanes and 19 by a warp.
+        const long long rows = static_cast<long long>(p.N) * p.H_q;
+        const int parts = rows <= 2048 ? 4 : 1;
+        const dim3 grid(static_cast<unsigned>((rows * parts + 31) / 32));
+        return p.d == 128 ? launch(span_merge_shared_kernel<128>, grid, stream, p, own, parts) : launch(span_merge_shared_kernel<64>, grid, stream, p, own, parts);
     }
-    // A cut unit's rows: with few of them a warp or two each, with 256 enough warps that each has one or two.
-    const dim3 grid(p.G, p.unit_rows <= 16 ? 1 : p.unit_rows / 16);
-    return p.d == 128 ? launch(span_merge_cross_kernel<4>, grid, stream, p) : launch(span_merge_cross_kernel<2>, grid, stream, p);
+    const int slices = (p.unit_rows + 3) / 4;  // warps that take a full unit's rows at once
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.G) * slices + 7) / 8));
+    return p.d == 128 ? launch(span_merge_cross_kernel<128>, grid, stream, p, slices) : launch(span_merge_cross_kernel<64>, grid, stream, p, slices);
 }
 
 }  // namespace gqa

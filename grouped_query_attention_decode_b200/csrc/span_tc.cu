@@ -217,6 +217,8 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
     if (warp == 0) {
         tmem_alloc(&sm->tmem_base, C::TMEM_COLS);
         tmem_relinquish();
+    } else if (warp == 1 && lane < 10) {
+        prefetch_tmap(&maps.q_shared + lane);  // the ten of SpanMaps, in a row
     }
     // Everything below reads what the kernels before on the stream wrote.
     grid_dependency_wait();
@@ -664,7 +666,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
         // ------------------------------------------------------------------ planner
         if (lane == 0) {
             const SpanRange cr = sm->range;
-            open_notes(p, cr, blockIdx.x);
+            open_notes(p, blockIdx.x);
             SpanWalker w;
             w.init(p, cr);
             SpanPiece piece;

@@ -5,7 +5,8 @@
 // sequence) against the rows they all attend -- or one sequence's own rows.  Per key/value head
 // a span's query rows are (token, query head of the group) pairs; they are cut into units of up
 // to `blk` tokens and rb heads, and a unit's cached rows into tiles of T.  As in schedule.cuh
-// the tiles of all units form one line, CTA i of G takes the tiles
+// the tiles of all units form one line, CTA i of G (of as many as there are tiles, if fewer) takes
+// the tiles
 //     [floor(i * total / G), floor((i + 1) * total / G)),
 // and every CTA derives its range from the lengths on the device.  A unit that lies in one CTA's
 // range is whole; the pieces of the others go to workspace slots (two per CTA: only a range's
@@ -47,16 +48,16 @@ struct SpanParams {
     int32_t *status;
     // workspace
     int4 *uinfo;           // own spans present: [unit] (first CTA, its slot, last CTA, 0)
-    struct SpanRecord *rec;  // no own spans: [CTA] the cut unit that starts there; else [0].total
+    struct SpanRecord *rec;  // no own spans: [CTA] the cut unit that starts there
     float *slots;          // [2 * G][slot_floats]
     long long slot_floats;
     float *res, *res_ml;   // [2][N * H_q][d] sums and [2][N * H_q][2] (m, l) of whole units
+    int behind_shared;     // span_few.cu: launched behind the launch over the shared spans
     int u1;                // number of the own spans' first token block, after the shared spans'
     int unit_rows;         // query rows of a slot
 };
 
 struct SpanRecord {
-    long long total;
     int valid, tok0, ntok, kvh, hb, k0, c1, pad;
 };
 
@@ -141,7 +142,18 @@ __device__ __forceinline__ int unit_number(const SpanParams &p, int s, const Spa
 struct SpanRange {
     long long begin, end, total, off0;
     int s0;
+    int parts;  // CTAs that have tiles, the first of them: min(G, total)
 };
+
+// Worker `cta`'s share of `total` tiles.
+__device__ __forceinline__ void share_of(const SpanParams &p, int cta, SpanRange &r) {
+    r.parts = static_cast<int>(r.total < p.G ? r.total : p.G);
+    const bool some = cta < r.parts;
+    r.begin = some ? cta_range_begin(cta, r.total, r.parts) : 0;
+    r.end = some ? cta_range_begin(cta + 1, r.total, r.parts) : 0;
+    r.s0 = 0;
+    r.off0 = 0;
+}
 
 // Whole CTA of NT threads: the total number of tiles, this CTA's range and the span it starts
 // in.  `scratch`: NT / 32 long longs of shared memory; `res`: shared.
@@ -161,19 +173,18 @@ __device__ void locate_span_range(const SpanParams &p, int cta, long long *scrat
         if (w < warp) off += scratch[w];
         total += scratch[w];
     }
-    const long long begin = cta_range_begin(cta, total, p.G), end = cta_range_begin(cta + 1, total, p.G);
-    if (tid == 0) {
-        res->begin = begin;
-        res->end = end;
-        res->total = total;
-        if (begin >= end) res->s0 = 0, res->off0 = 0;
-    }
-    if (begin < end && off <= begin && begin < off + mine) {
+    SpanRange mine_r;
+    mine_r.total = total;
+    share_of(p, cta, mine_r);
+    const long long begin = mine_r.begin;
+    if (tid == 0 && begin >= mine_r.end) *res = mine_r;
+    if (begin < mine_r.end && off <= begin && begin < off + mine) {
         for (int s = s0; s < s1; ++s) {
             const long long v = span_tiles(p, span_at(p, s, false));
             if (begin < off + v) {
-                res->s0 = s;
-                res->off0 = off;
+                mine_r.s0 = s;
+                mine_r.off0 = off;
+                *res = mine_r;
                 break;
             }
             off += v;
@@ -182,32 +193,45 @@ __device__ void locate_span_range(const SpanParams &p, int cta, long long *scrat
     __syncthreads();
 }
 
-// The same by one warp, for worker `cta`.
-__device__ inline SpanRange locate_span_range_warp(const SpanParams &p, int cta, int lane) {
-    SpanRange r = {0, 0, 0, 0, 0};
-    for (int s0 = p.s_begin; s0 < p.s_end; s0 += 32) {
-        const int s = s0 + lane;
-        const long long v = s < p.s_end ? span_tiles(p, span_at(p, s, cta == 0)) : 0;
-        r.total += __shfl_sync(kFullMask, warp_incl_scan(v, lane), 31);
+// The same for a CTA whose warps are workers of their own: called by all NT threads, it gives every
+// warp the range of its worker.  `before`: NT long longs of shared memory, `scratch` NT / 32.
+template <int NT>
+__device__ SpanRange locate_warp_ranges(const SpanParams &p, int worker, bool flag, long long *before, long long *scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.s_end - p.s_begin + NT - 1) / NT;
+    const int s0 = p.s_begin + tid * per, s1 = min(p.s_end, s0 + per);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += span_tiles(p, span_at(p, s, flag));
+    const long long incl = warp_incl_scan(mine, lane);
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long off = incl - mine;
+    SpanRange r = {};
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) off += scratch[w];
+        r.total += scratch[w];
     }
-    r.begin = cta_range_begin(cta, r.total, p.G);
-    r.end = cta_range_begin(cta + 1, r.total, p.G);
+    before[tid] = off;
+    __syncthreads();
+    share_of(p, worker, r);
     if (r.begin >= r.end) return r;
-    long long off = 0;
-    for (int s0 = p.s_begin; s0 < p.s_end; s0 += 32) {
-        const int s = s0 + lane;
-        const long long v = s < p.s_end ? span_tiles(p, span_at(p, s, false)) : 0;
-        const long long incl = warp_incl_scan(v, lane);
-        const uint32_t m = __ballot_sync(kFullMask, off + incl - v <= r.begin && r.begin < off + incl);
-        if (m != 0) {
-            const int l = __ffs(m) - 1;
-            r.s0 = s0 + l;
-            r.off0 = off + __shfl_sync(kFullMask, incl - v, l);
-            return r;
-        }
-        off += __shfl_sync(kFullMask, incl, 31);
+    // the last thread whose spans start at or before the range's first tile holds it (of several
+    // that start there, all but the last are empty)
+    int t = -1;
+    for (int b = 0; b < NT; b += 32) {
+        const uint32_t m = __ballot_sync(kFullMask, before[b + lane] <= r.begin);
+        if (m != 0) t = b + 31 - __clz(m);
+        if (m != kFullMask) break;
     }
-    return r;  // unreachable when begin < total
+    r.off0 = before[t];
+    for (int s = p.s_begin + t * per; s < min(p.s_end, p.s_begin + (t + 1) * per); ++s) {
+        const long long v = span_tiles(p, span_at(p, s, false));
+        r.s0 = s;
+        if (r.begin < r.off0 + v) break;
+        r.off0 += v;
+    }
+    return r;
 }
 
 // One CTA-range piece of one unit.
@@ -294,19 +318,18 @@ __device__ __forceinline__ int seen_rows(const SpanParams &p, const SpanSegment 
 }
 
 // One thread of worker `cta` (a CTA, or a warp of span_few.cu), before its segments.
-__device__ __forceinline__ void open_notes(const SpanParams &p, const SpanRange &cr, int cta) {
+__device__ __forceinline__ void open_notes(const SpanParams &p, int cta) {
     if (p.B == 0) p.rec[cta].valid = 0;
-    else if (cta == 0) p.rec[0].total = cr.total;
 }
 
 // The same thread, once per segment: what the merge needs to find the unit's pieces.
 __device__ inline void note_unit(const SpanParams &p, const SpanSegment &g, const SpanRange &cr, int c0) {
     if (g.j0 != 0) return;
-    const int c1 = g.whole() ? c0 : static_cast<int>(cta_of_tile(g.uoff + g.nt - 1, cr.total, p.G));
+    const int c1 = g.whole() ? c0 : static_cast<int>(cta_of_tile(g.uoff + g.nt - 1, cr.total, cr.parts));
     if (p.B > 0) {  // there are own rows to join with, here or in another launch
         p.uinfo[g.unit] = make_int4(c0, g.first ? 0 : 1, c1, 0);
     } else if (!g.whole()) {
-        p.rec[c0] = SpanRecord{cr.total, 1, g.tok0, g.ntok, g.kvh, g.hb, g.first ? 0 : 1, c1, 0};
+        p.rec[c0] = SpanRecord{1, g.tok0, g.ntok, g.kvh, g.hb, g.first ? 0 : 1, c1, 0};
     }
 }
 
