@@ -723,7 +723,13 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
                                         static_cast<const float *>(a.v_own), stream);
         return res != GQA_OK ? res : launch_span_merge(p, p, stream);
     }
+    if (encode_fn() == nullptr) return GQA_ERR_CUDA;
+    // caches as (d, H_kv, rows, prefixes or sequences) or (d, H_kv, page_size, n_pages)
+    const int rows_g = paged ? a.page_size : a.g_max, rows_o = paged ? a.page_size : a.own_max;
+    const int outer_g = paged ? a.n_pages : a.P, outer_o = paged ? a.n_pages : a.B;
+    const int box = paged && a.page_size < s.T ? a.page_size : s.T;
     SpanParams fp = p;
+    CUtensorMap few_k, few_v;
     if (s.few) {
         fp.rb = s.few_rb;
         fp.HB = 1;
@@ -736,18 +742,17 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
         fp.uinfo = reinterpret_cast<int4 *>(w + s.few_uinfo);
         fp.slots = reinterpret_cast<float *>(w + s.few_slots);
         fp.slot_floats = kFewRows * (a.d + 2);
-        if (a.B == 0) {
-            const int rc2 = launch_span_few(fp, a.q, a.k_shared, a.v_shared, stream);
+        const bool own = a.B > 0;
+        if (!encode_cache_map(&few_k, own ? a.k_own : a.k_shared, own ? outer_o : outer_g, a.H_kv, a.d, own ? rows_o : rows_g, 8) ||
+            !encode_cache_map(&few_v, own ? a.v_own : a.v_shared, own ? outer_o : outer_g, a.H_kv, a.d, own ? rows_o : rows_g, 8))
+            return GQA_ERR_SHAPE;
+        if (!own) {
+            const int rc2 = launch_span_few(fp, few_k, few_v, a.q, stream);
             return rc2 != GQA_OK ? rc2 : launch_span_merge(fp, fp, stream);
         }
         p.s_end = fp.s_begin = a.P;
         fp.behind_shared = 1;
     }
-    if (encode_fn() == nullptr) return GQA_ERR_CUDA;
-    // caches as (d, H_kv, rows, prefixes or sequences) or (d, H_kv, page_size, n_pages)
-    const int rows_g = paged ? a.page_size : a.g_max, rows_o = paged ? a.page_size : a.own_max;
-    const int outer_g = paged ? a.n_pages : a.P, outer_o = paged ? a.n_pages : a.B;
-    const int box = paged && a.page_size < s.T ? a.page_size : s.T;
     SpanMaps m;
     if (!encode_q_map(&m.q_shared, a.q, a.N, s.tb, a.H_q, a.d, s.rb) ||
         !encode_cache_map(&m.k_shared, a.k_shared, outer_g, a.H_kv, a.d, rows_g, box) ||
@@ -769,7 +774,7 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
          !encode_cache_map(&m.v_own8, a.v_own, outer_o, a.H_kv, a.d, rows_o, 8)))
         return GQA_ERR_SHAPE;
     int res = launch_span_tc(m, p, stream);
-    if (res == GQA_OK && s.few) res = launch_span_few(fp, a.q, a.k_own, a.v_own, stream);
+    if (res == GQA_OK && s.few) res = launch_span_few(fp, few_k, few_v, a.q, stream);
     return res != GQA_OK ? res : launch_span_merge(p, fp, stream);
 }
 

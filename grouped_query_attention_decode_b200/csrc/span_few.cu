@@ -24,24 +24,21 @@ namespace gqa {
 
 namespace {
 
+constexpr unsigned long long kFewDrainNs = 1000000000ull;
+
 template <int D>
 struct FewCfg {
     static constexpr int T = 16;                 // rows of a tile
-    static constexpr int CH = D / 8;             // 16-byte chunks of a row
-    static constexpr int TILE = T * D * 2;       // bytes of a K or V tile
+    static constexpr int KB = D / 64;            // 128-byte column blocks of a row
+    static constexpr int TILE = T * D * 2;       // bytes of a K or V tile: KB blocks of 16 rows of 128 bytes
     static constexpr int S = 3;                  // tiles of a warp's ring
     static constexpr int WARPS = D == 128 ? 8 : 16;
-    static constexpr int SMEM_BYTES = WARPS * S * 2 * TILE;
+    static constexpr int BOXES = 4 * KB;         // copies of a tile: K or V, 8 rows, a column block
+    static constexpr int RING_BYTES = WARPS * S * 2 * TILE;
+    static constexpr int BAR_BYTES = (WARPS * S * 8 + 127) / 128 * 128;
+    static constexpr int SMEM_BYTES = RING_BYTES + BAR_BYTES + WARPS * 33 * 8;  // and locate_warp_ranges' sums
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
-
-// 16 bytes from global to shared memory; zeros when `some` is false.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -66,24 +63,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(FewCfg<D>::WARPS * 32, 1)
-span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ kc,
-                const __nv_bfloat16 *__restrict__ vc, const __grid_constant__ SpanParams p) {
+span_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __nv_bfloat16 *__restrict__ q, const __grid_constant__ SpanParams p) {
     using C = FewCfg<D>;
-    constexpr int T = C::T, CH = C::CH, S = C::S;
-    extern __shared__ __align__(128) uint8_t few_smem[];
-    const int lane = threadIdx.x & 31;
-    const int worker = blockIdx.x * C::WARPS + (threadIdx.x >> 5);
-    const uint32_t ring = smem_u32(few_smem) + (threadIdx.x >> 5) * (S * 2 * C::TILE);
+    constexpr int T = C::T, S = C::S, KB = C::KB;
+    extern __shared__ __align__(1024) uint8_t few_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int worker = blockIdx.x * C::WARPS + warp;
+    uint8_t *const ring = few_smem + warp * (S * 2 * C::TILE);
+    uint64_t *const full = reinterpret_cast<uint64_t *>(few_smem + C::RING_BYTES) + warp * S;
+    if ((smem_u32(few_smem) & 1023u) != 0) {
+        if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, GQA_STATUS_INTERNAL);
+        return;
+    }
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(full + i, 1);
+        fence_mbarrier_init();
+    }
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
 
     // Behind the launch over the shared rows nothing here depends on it: what that launch waited for
     // before it let this one start is all that is read.  The launch behind this one has to find both
     // complete, so the wait comes at the end.
     if (!p.behind_shared) grid_dependency_wait();
     grid_launch_dependents();
-    // in the ring, which nothing uses yet
-    auto *const before = reinterpret_cast<long long *>(few_smem);
+    auto *const before = reinterpret_cast<long long *>(few_smem + C::RING_BYTES + C::BAR_BYTES);
     const SpanRange cr = locate_warp_ranges<C::WARPS * 32>(p, worker, blockIdx.x == 0, before, before + C::WARPS * 32);
-    __syncthreads();
     if (lane == 0) open_notes(p, worker);
 
     // The copies run S - 1 tiles ahead, with a walker of their own.
@@ -93,69 +101,62 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
     int cj = 0;
     bool copies_left = cw.next(p, cg);
     int n_copied = 0;
-    // 16-row tiles start on multiples of 8 rows of the table, so a tile has at most two pages.  Their
-    // numbers are read when the copy before is issued.
-    int pages[2];
+    // Lane i < BOXES copies one box of a tile: K or V, a column block, its first or last 8 rows.
+    // A box lies in one page (pages hold multiples of 8 rows and tiles start at multiples of 8);
+    // the page's number is read when the copy before is issued.
+    const bool is_v = lane & 1;
+    const int cb = KB == 2 ? (lane >> 1) & 1 : 0, half = lane / (2 * KB);
+    uint8_t *const to = ring + (is_v ? C::TILE : 0) + cb * 2048 + half * 1024;
+    const uint64_t once = l2_policy_evict_first();
+    int row, outer;  // of the box
     auto look_up = [&]() {
+        if (!copies_left) return;
+        const int t0 = (cg.j0 + cj) * T + 8 * half;
+        row = cg.row0 + t0;
+        outer = cg.src;
         if constexpr (PAGED) {
-            const int t0 = (cg.j0 + cj) * T;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                pages[h] = copies_left && t0 + 8 * h < cg.rows
-                               ? __ldg(p.block_table + static_cast<long long>(cg.src) * p.max_pages + (cg.row0 + t0 + 8 * h) / p.page_size)
-                               : 0;
+            if (lane < C::BOXES && t0 < cg.rows) {
+                const int i = row / p.page_size;
+                outer = __ldg(p.block_table + static_cast<long long>(cg.src) * p.max_pages + i);
+                row -= i * p.page_size;
+            }
         }
     };
     look_up();
     auto copy_tile = [&]() {
-        if (copies_left) {
-            const int t0 = (cg.j0 + cj) * T, rows = cg.rows - t0;  // rows left from here on
-            const uint32_t dst = ring + (n_copied % S) * (2 * C::TILE);
-            long long base[2];
-            if constexpr (PAGED) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = cg.row0 + t0 + 8 * h;
-                    int pg = pages[h];
-                    if (pg < 0 || pg >= p.n_pages) {
-                        if (p.status != nullptr) atomicOr(p.status, GQA_STATUS_PAGE_RANGE);
-                        pg = 0;
-                    }
-                    base[h] = static_cast<long long>(pg) * p.page_size + row % p.page_size - 8 * h;
-                }
-            } else {
-                base[0] = base[1] = static_cast<long long>(cg.src) * (cg.s < p.P ? p.g_max : p.own_max) + cg.row0 + t0;
+        if (!copies_left) return;
+        const int st = n_copied % S, rows = cg.rows - (cg.j0 + cj) * T;  // rows left from the tile's first on
+        if (lane == 0) mbar_arrive_expect_tx(full + st, (rows > 8 ? 2 : 1) * 2 * KB * 1024);
+        __syncwarp();
+        if (lane < C::BOXES && 8 * half < rows) {
+            if (PAGED && (outer < 0 || outer >= p.n_pages)) {
+                if (p.status != nullptr) atomicOr(p.status, GQA_STATUS_PAGE_RANGE);
+                outer = 0;
             }
-            constexpr int STEP = 32 / CH;  // rows per instruction
-            const int r0 = lane / CH, c = lane % CH;
-            const long long stride = static_cast<long long>(p.H_kv) * D;
-#pragma unroll
-            for (int i = 0; i < T / STEP; ++i) {
-                const int r = i * STEP + r0;
-                const bool some = r < rows;
-                const long long at = some ? (base[i * STEP >= 8] + r) * stride + cg.kvh * D + c * 8 : 0;
-                const uint32_t to = dst + r * (D * 2) + ((c ^ (r & 7)) << 4);
-                copy16(to, kc + at, some);
-                copy16(to + C::TILE, vc + at, some);
-            }
-            ++n_copied;
-            if (++cj == cg.len) {
-                copies_left = cw.next(p, cg);
-                cj = 0;
-            }
-            look_up();
+            tma_load_4d(to + st * (2 * C::TILE), is_v ? &tm_v : &tm_k, full + st, cb * 64, cg.kvh, row, outer, once);
         }
-        copy_commit();  // an empty group keeps the count
+        ++n_copied;
+        if (++cj == cg.len) {
+            copies_left = cw.next(p, cg);
+            cj = 0;
+        }
+        look_up();
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < S - 1; ++i) copy_tile();
 
     SpanWalker w;
     w.init(p, cr);
     SpanSegment g;
     int n = 0;
-    const float neg = p.negate ? -1.f : 1.f;
-    while (w.next(p, g)) {
+    bool ok = true;
+    const float scale = p.negate ? -p.scale_log2 : p.scale_log2;
+    // ldmatrix rows and 16-byte chunks of this lane: K as it lies (rows are the second operand's
+    // columns), V transposed; chunk c of row r stands at c ^ (r % 8)
+    const int kr = (lane >> 4) * 8 + (lane & 7), vr = ((lane >> 3) & 1) * 8 + (lane & 7);
+    const uint32_t k_at = smem_u32(ring) + kr * 128 + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+    const uint32_t v_at = smem_u32(ring) + C::TILE + vr * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+    while (ok && w.next(p, g)) {
         if (lane == 0) note_unit(p, g, cr, worker);
         // This thread's query rows are lane / 4 and lane / 4 + 8; its q values, as the first operand
         // of the score product, are columns 16 k + 2 (lane % 4) .. + 1 and + 8 of both.
@@ -175,27 +176,34 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
             }
         }
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float o[D / 8][4];
+        float2 o[D / 8][2];  // [8 columns][row]
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = make_float2(0.f, 0.f);
 
         for (int jj = 0; jj < g.len; ++jj, ++n) {
-            copy_wait<S - 2>();
-            __syncwarp();  // the tile is there for everyone, and everyone has left the one before
-            copy_tile();
-            const uint32_t kt = ring + (n % S) * (2 * C::TILE), vt = kt + C::TILE;
+            const int st = n % S;
+            ok = __all_sync(kFullMask, wait_bounded(full + st, (n / S) & 1, nullptr, p.wait_ns));
+            if (!ok) break;
+            copy_tile();  // into the slot of the tile before, which everyone has left
+            const uint32_t off = st * (2 * C::TILE);
+            const int t0 = (g.j0 + jj) * T;
+            if (g.rows - t0 < T) {
+                // rows past the end: their weights are 0, but what stands there may be NaN or infinite
+                for (int i = (g.rows - t0) * 8 + lane; i < T * 8; i += 32)
+#pragma unroll
+                    for (int b = 0; b < KB; ++b)
+                        *reinterpret_cast<uint4 *>(ring + off + C::TILE + b * 2048 + i * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();  // before a later copy into the slot
+                __syncwarp();
+            }
             float s[2][4] = {};
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint32_t b[4];
-                const int r = (lane >> 4) * 8 + (lane & 7), c = 2 * k + ((lane >> 3) & 1);
-                ldmatrix4(b, kt + r * (D * 2) + ((c ^ (r & 7)) << 4));
+                ldmatrix4(b, (k_at + off + (k >> 2) * 2048) ^ ((k & 3) << 5));
                 mma(s[0], qa[k], b[0], b[1]);
                 mma(s[1], qa[k], b[2], b[3]);
             }
-            const int t0 = (g.j0 + jj) * T;
             float pr[2][2][2];  // [row][8 columns][value]
             bool raise = false;
             float m_new[2];
@@ -207,7 +215,7 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const bool in = t0 + 8 * x + 2 * (lane & 3) + e < seen[h];
-                        pr[h][x][e] = in ? s[x][2 * h + e] * (neg * p.scale_log2) : -INFINITY;
+                        pr[h][x][e] = in ? s[x][2 * h + e] * scale : -INFINITY;
                         top = fmaxf(top, pr[h][x][e]);
                     }
                 top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
@@ -223,8 +231,8 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
                     l[h] *= alpha;
 #pragma unroll
                     for (int j = 0; j < D / 8; ++j) {
-                        o[j][2 * h] *= alpha;
-                        o[j][2 * h + 1] *= alpha;
+                        o[j][h].x *= alpha;
+                        o[j][h].y *= alpha;
                     }
                 }
             }
@@ -243,18 +251,18 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 uint32_t b[4];
-                const int r = ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * j + (lane >> 4);
-                ldmatrix4_t(b, vt + r * (D * 2) + ((c ^ (r & 7)) << 4));
+                ldmatrix4_t(b, (v_at + off + (j >> 2) * 2048) ^ ((j & 3) << 5));
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float t[4] = {};
                     mma(t, lo, b[2 * x], b[2 * x + 1]);
                     mma(t, hi, b[2 * x], b[2 * x + 1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[2 * j + x][e] += t[e];
+                    o[2 * j + x][0] = add_f32x2(o[2 * j + x][0], make_float2(t[0], t[1]));
+                    o[2 * j + x][1] = add_f32x2(o[2 * j + x][1], make_float2(t[2], t[3]));
                 }
             }
         }
+        if (!ok) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             l[h] += __shfl_xor_sync(kFullMask, l[h], 1);
@@ -281,8 +289,13 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
             if (ml != nullptr && lane % 4 == 0) *reinterpret_cast<float2 *>(ml) = make_float2(m[h], l[h]);
 #pragma unroll
             for (int j = 0; j < D / 8; ++j)
-                *reinterpret_cast<float2 *>(dst + 8 * j + 2 * (lane % 4)) = make_float2(o[j][2 * h] * norm, o[j][2 * h + 1] * norm);
+                *reinterpret_cast<float2 *>(dst + 8 * j + 2 * (lane % 4)) = make_float2(o[j][h].x * norm, o[j][h].y * norm);
         }
+    }
+    if (!ok) {
+        if (lane == 0 && p.status != nullptr) atomicOr(p.status, GQA_STATUS_WAIT_TIMEOUT);
+        // no copy may still be writing this CTA's shared memory when it exits
+        for (int i = n; i < n_copied; ++i) wait_bounded(full + i % S, (i / S) & 1, nullptr, kFewDrainNs);
     }
     if (p.behind_shared) grid_dependency_wait();
 }
@@ -290,7 +303,7 @@ span_few_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__rest
 namespace {
 
 template <int D, bool PAGED>
-int launch_span_few_impl(const SpanParams &p, const void *q, const void *k, const void *v, cudaStream_t stream) {
+int launch_span_few_impl(const SpanParams &p, const CUtensorMap &k, const CUtensorMap &v, const void *q, cudaStream_t stream) {
     using C = FewCfg<D>;
     auto kern = span_few_kernel<D, PAGED>;
     static bool attr_set[64] = {};
@@ -311,9 +324,7 @@ int launch_span_few_impl(const SpanParams &p, const void *q, const void *k, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(k),
-                           static_cast<const __nv_bfloat16 *>(v), p) != cudaSuccess)
-        return GQA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, k, v, static_cast<const __nv_bfloat16 *>(q), p) != cudaSuccess) return GQA_ERR_CUDA;
     return GQA_OK;
 }
 
@@ -321,10 +332,10 @@ int launch_span_few_impl(const SpanParams &p, const void *q, const void *k, cons
 
 int span_few_warps(int d) { return d == 128 ? FewCfg<128>::WARPS : FewCfg<64>::WARPS; }
 
-int launch_span_few(const SpanParams &p, const void *q, const void *k, const void *v, cudaStream_t stream) {
+int launch_span_few(const SpanParams &p, const CUtensorMap &k, const CUtensorMap &v, const void *q, cudaStream_t stream) {
     if (p.block_table != nullptr)
-        return p.d == 128 ? launch_span_few_impl<128, true>(p, q, k, v, stream) : launch_span_few_impl<64, true>(p, q, k, v, stream);
-    return p.d == 128 ? launch_span_few_impl<128, false>(p, q, k, v, stream) : launch_span_few_impl<64, false>(p, q, k, v, stream);
+        return p.d == 128 ? launch_span_few_impl<128, true>(p, k, v, q, stream) : launch_span_few_impl<64, true>(p, k, v, q, stream);
+    return p.d == 128 ? launch_span_few_impl<128, false>(p, k, v, q, stream) : launch_span_few_impl<64, false>(p, k, v, q, stream);
 }
 
 }  // namespace gqa

@@ -348,8 +348,9 @@ int launch_span_f32(const SpanParams &p, const float *q, const float *ks, const 
 // Joins the pieces of one launch over the shared spans and one over the own ones (the same launch,
 // or none: own.B = 0).
 int launch_span_merge(const SpanParams &shared, const SpanParams &own, cudaStream_t stream);
-// The kernel for few query rows per span; p.G is the number of warps (span_few_warps a CTA).
-int launch_span_few(const SpanParams &p, const void *q, const void *k, const void *v, cudaStream_t stream);
+// The kernel for few query rows per span; p.G is the number of warps (span_few_warps a CTA), k and v
+// are copied in boxes of 8 rows.
+int launch_span_few(const SpanParams &p, const CUtensorMap &k, const CUtensorMap &v, const void *q, cudaStream_t stream);
 int span_few_warps(int d);
 
 }  // namespace gqa
