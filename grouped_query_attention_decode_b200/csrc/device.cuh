@@ -415,6 +415,13 @@ __device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
     return d;
 }
 
+// One 32-byte store (32-byte aligned).
+__device__ __forceinline__ void st_global_v8(float *p, const float (&v)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+                 "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -192,28 +192,28 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
         if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, GQA_STATUS_INTERNAL);
         return;
     }
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&sm->full[s], 1);
-            mbar_init(&sm->empty[s], 2);  // the issuer's use of the slot and warp 2's look at it
-            mbar_init(&sm->fixed[s], 1);
-        }
-        for (int j = 0; j < 2; ++j) {
-            mbar_init(&sm->q_full[j], 1);
-            mbar_init(&sm->q_empty[j], 1);
-            mbar_init(&sm->s_full[j], 1);
-            mbar_init(&sm->p_full[j], 4);
-            mbar_init(&sm->o_full[j], 1);
-        }
-        for (int j = 0; j < kPieces; ++j) {
-            mbar_init(&sm->piece_full[j], 1);
-            mbar_init(&sm->piece_empty[j], 11);  // warps 0..2 and the softmax warps
-        }
-        for (int w = 0; w < 4; ++w) mbar_init(&sm->joined[w], 2);
+    // a few barriers to a thread: one thread takes a thousand cycles for all of them
+    const int t = threadIdx.x - 64;
+    if (t >= 0 && t < S) {
+        mbar_init(&sm->full[t], 1);
+        mbar_init(&sm->empty[t], 2);  // the issuer's use of the slot and warp 2's look at it
+        mbar_init(&sm->fixed[t], 1);
+    } else if (t >= 16 && t < 18) {
+        mbar_init(&sm->q_full[t - 16], 1);
+        mbar_init(&sm->q_empty[t - 16], 1);
+        mbar_init(&sm->s_full[t - 16], 1);
+        mbar_init(&sm->p_full[t - 16], 4);
+        mbar_init(&sm->o_full[t - 16], 1);
+    } else if (t >= 20 && t < 20 + kPieces) {
+        mbar_init(&sm->piece_full[t - 20], 1);
+        mbar_init(&sm->piece_empty[t - 20], 11);  // warps 0..2 and the softmax warps
+    } else if (t >= 24 && t < 28) {
+        mbar_init(&sm->joined[t - 24], 2);
+    } else if (t == 28) {
         mbar_init(&sm->mma_done, 1);
         sm->abort = 0;
-        fence_mbarrier_init();
     }
+    if (t >= 0 && t < 32) fence_mbarrier_init();
     if (warp == 0) {
         tmem_alloc(&sm->tmem_base, C::TMEM_COLS);
         tmem_relinquish();
@@ -465,11 +465,26 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 if (dst_ml != nullptr && c0 == 0) *reinterpret_cast<float2 *>(dst_ml) = make_float2(m, l);
                 const float norm = whole && p.B == 0 ? 1.f / l : 1.f;
                 dst += c0;
+                // A thread writes its own row, so every store instruction touches 32 lines, which is
+                // what it costs: 32 bytes at a time where the row is aligned (the workspace is; out
+                // may not be).
+                const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll
-                for (int c = 0; c < D; c += 4)
-                    if (c < c1 - c0)
-                        __stcg(reinterpret_cast<float4 *>(dst + c),
-                               make_float4(o2[c / 2].x * norm, o2[c / 2].y * norm, o2[c / 2 + 1].x * norm, o2[c / 2 + 1].y * norm));
+                for (int c = 0; c < D; c += 8)
+                    if (c < c1 - c0) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            v[e] = o2[(c + e) / 2].x * norm;
+                            v[e + 1] = o2[(c + e) / 2].y * norm;
+                        }
+                        if (wide) {
+                            st_global_v8(dst + c, v);
+                        } else {
+                            *reinterpret_cast<float4 *>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<float4 *>(dst + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
             }
         }
         if (!ok && lane == 0) fail();
@@ -675,7 +690,6 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 more = w.next(p, piece.g);
                 piece.pair = piece.last_rows = piece.steps = 0;
                 if (more) {
-                    note_unit(p, piece.g, cr, blockIdx.x);
                     piece.pair = piece.g.ntok > p.tb;
                     piece.steps = piece.pair ? 2 * piece.g.len : piece.g.len;
                     piece.last_rows = min(T, piece.g.rows - (piece.g.j0 + piece.g.len - 1) * T);
@@ -684,6 +698,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 if (ok) {
                     sm->piece[i % kPieces] = piece;
                     mbar_arrive(&sm->piece_full[i % kPieces]);
+                    if (more) note_unit(p, piece.g, cr, blockIdx.x);
                 }
             }
             if (!ok) fail();

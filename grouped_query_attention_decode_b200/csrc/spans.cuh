@@ -75,7 +75,7 @@ __device__ __forceinline__ int group_of(const SpanParams &p, int i) {
 // Rows group g shares, or -1 when the entry is out of range.
 __device__ __forceinline__ int shared_rows_of(const SpanParams &p, int g) {
     const int n = __ldg(p.glen + g);
-    return n < 0 || n > p.g_max || n % p.g_step != 0 ? -1 : n;
+    return n < 0 || n > p.g_max || (p.g_step > 1 && n % p.g_step != 0) ? -1 : n;
 }
 
 // First own row and number of own rows of sequence b; false when its length (or its group's) is
@@ -103,11 +103,11 @@ __device__ inline Span span_at(const SpanParams &p, int s, bool flag) {
     Span sp = {0, 0, 0, 0, 0};
     int bad = 0;
     if (s < p.P) {
-        const int a = __ldg(p.gstart + s), e = __ldg(p.gstart + s + 1);
+        // all three reads at once: every caller waits for them
+        const int a = __ldg(p.gstart + s), e = __ldg(p.gstart + s + 1), n = shared_rows_of(p, s);
         if (a < 0 || e < a || e > (p.B > 0 ? p.B : p.N)) {
             bad = GQA_STATUS_GROUP_RANGE;
         } else {
-            const int n = shared_rows_of(p, s);
             if (n < 0) bad = GQA_STATUS_SEQLEN_RANGE;
             sp.tok0 = a * p.Q;
             sp.ntok = (e - a) * p.Q;
@@ -143,6 +143,7 @@ struct SpanRange {
     long long begin, end, total, off0;
     int s0;
     int parts;  // CTAs that have tiles, the first of them: min(G, total)
+    Span span;  // span s0
 };
 
 // Worker `cta`'s share of `total` tiles.
@@ -153,6 +154,7 @@ __device__ __forceinline__ void share_of(const SpanParams &p, int cta, SpanRange
     r.end = some ? cta_range_begin(cta + 1, r.total, r.parts) : 0;
     r.s0 = 0;
     r.off0 = 0;
+    r.span = Span{0, 0, 0, 0, 0};
 }
 
 // Whole CTA of NT threads: the total number of tiles, this CTA's range and the span it starts
@@ -163,7 +165,11 @@ __device__ void locate_span_range(const SpanParams &p, int cta, long long *scrat
     const int per = (p.s_end - p.s_begin + NT - 1) / NT;
     const int s0 = p.s_begin + tid * per, s1 = min(p.s_end, s0 + per);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += span_tiles(p, span_at(p, s, cta == 0));
+    Span sp = {0, 0, 0, 0, 0};
+    for (int s = s0; s < s1; ++s) {
+        sp = span_at(p, s, cta == 0);
+        mine += span_tiles(p, sp);
+    }
     const long long incl = warp_incl_scan(mine, lane);
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
@@ -180,10 +186,12 @@ __device__ void locate_span_range(const SpanParams &p, int cta, long long *scrat
     if (tid == 0 && begin >= mine_r.end) *res = mine_r;
     if (begin < mine_r.end && off <= begin && begin < off + mine) {
         for (int s = s0; s < s1; ++s) {
-            const long long v = span_tiles(p, span_at(p, s, false));
+            if (per > 1) sp = span_at(p, s, false);
+            const long long v = span_tiles(p, sp);
             if (begin < off + v) {
                 mine_r.s0 = s;
                 mine_r.off0 = off;
+                mine_r.span = sp;
                 *res = mine_r;
                 break;
             }
@@ -226,7 +234,8 @@ __device__ SpanRange locate_warp_ranges(const SpanParams &p, int worker, bool fl
     }
     r.off0 = before[t];
     for (int s = p.s_begin + t * per; s < min(p.s_end, p.s_begin + (t + 1) * per); ++s) {
-        const long long v = span_tiles(p, span_at(p, s, false));
+        r.span = span_at(p, s, false);
+        const long long v = span_tiles(p, r.span);
         r.s0 = s;
         if (r.begin < r.off0 + v) break;
         r.off0 += v;
@@ -253,8 +262,7 @@ struct SpanWalker {
     Span sp;
     bool opened;
 
-    __device__ void load(const SpanParams &p) {
-        sp = span_at(p, s, false);
+    __device__ void open(const SpanParams &p) {
         nt = tiles_of(sp.rows, p.T);
         nblk = span_blocks(p, sp);
     }
@@ -265,7 +273,8 @@ struct SpanWalker {
         s = cr.s0;
         opened = false;
         nt = nblk = 0;
-        if (t < end) load(p);
+        sp = cr.span;
+        if (t < end) open(p);
     }
     __device__ bool next(const SpanParams &p, SpanSegment &g) {
         if (t >= end) return false;
@@ -276,16 +285,17 @@ struct SpanWalker {
                 t = end;
                 return false;
             }
-            load(p);
+            sp = span_at(p, s, false);
+            open(p);
         }
         const long long rel = t - off;
         const int k = static_cast<int>(udiv(rel, nt));
-        const int h = k / nblk, block = k - h * nblk;
+        const int h = nblk == 1 ? k : k / nblk, block = k - h * nblk;
         g.s = s;
         g.src = sp.src;
         g.tok0 = sp.tok0 + block * p.blk;
         g.ntok = min(p.blk, sp.ntok - block * p.blk);
-        g.kvh = h / p.HB;
+        g.kvh = p.HB == 1 ? h : h / p.HB;
         g.hb = h - g.kvh * p.HB;
         g.row0 = sp.row0;
         g.rows = sp.rows;
