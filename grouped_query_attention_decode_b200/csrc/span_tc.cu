@@ -58,6 +58,7 @@ struct SpanPiece {
     int steps;      // 0: there are no more pieces
     int pair;       // two row tiles per cached tile
     int last_rows;  // rows of the piece's last tile
+    int once;       // no other unit reads these cached rows
 };
 
 template <int D>
@@ -528,7 +529,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 uint8_t *dst = ring + st * C::TILE_BYTES + lane * boxr * 128;
 #pragma unroll
                 for (int kb = 0; kb < C::KB; ++kb)
-                    tma_load_4d(dst + kb * T * 128, m, &sm->full[st], kb * 64, kvh, row, pg, shared ? again : once);
+                    tma_load_4d(dst + kb * T * 128, m, &sm->full[st], kb * 64, kvh, row, pg, pieces.at(c.i).once ? once : again);
             }
             ++n;
             return true;
@@ -690,6 +691,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
                 more = w.next(p, piece.g);
                 piece.pair = piece.last_rows = piece.steps = 0;
                 if (more) {
+                    piece.once = w.nblk == 1 && p.HB == 1;
                     piece.pair = piece.g.ntok > p.tb;
                     piece.steps = piece.pair ? 2 * piece.g.len : piece.g.len;
                     piece.last_rows = min(T, piece.g.rows - (piece.g.j0 + piece.g.len - 1) * T);
