@@ -73,6 +73,7 @@ span_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     uint8_t *const ring = few_smem + warp * (S * 2 * C::TILE);
     uint64_t *const full = reinterpret_cast<uint64_t *>(few_smem + C::RING_BYTES) + warp * S;
     if ((smem_u32(few_smem) & 1023u) != 0) {
+        grid_dependency_wait();
         if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, GQA_STATUS_INTERNAL);
         return;
     }

@@ -190,6 +190,7 @@ span_tc_kernel(const __grid_constant__ SpanMaps maps, const __grid_constant__ Sp
     const int lane = threadIdx.x & 31;
 
     if ((smem_u32(smem) & 1023u) != 0) {
+        grid_dependency_wait();  // what is launched behind counts on it
         if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, GQA_STATUS_INTERNAL);
         return;
     }

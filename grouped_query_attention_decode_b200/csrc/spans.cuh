@@ -19,6 +19,7 @@
 #include "device.cuh"
 #include "gqa.h"
 #include "schedule.cuh"
+#include "span_device.cuh"
 
 namespace gqa {
 

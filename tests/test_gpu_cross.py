@@ -152,3 +152,67 @@ def test_few_tokens_repeat():
     again, _ = run(x, 0.1, workspace=ws)
     assert torch.equal(first, again)
     check(x, first, 0.1)
+
+
+@pytest.mark.parametrize("tokens", [[1, 2, 1], [5, 70, 300]], ids=["few", "many"])
+def test_wait_timeout_is_reported_and_the_context_recovers(tokens):
+    x = make(tokens, [700, 333, 2000], (16, 4, 128), torch.bfloat16)
+    gqa.set_wait_timeout_ns(1)
+    try:
+        _, status = run(x, 0.1)
+    finally:
+        gqa.set_wait_timeout_ns(0)
+    # a warp of the kernel for few tokens waits for copies alone, which may be in before it looks twice
+    assert status & gqa.STATUS_WAIT_TIMEOUT or (status == 0 and sum(tokens) < 10)
+    out, status = run(x, 0.1)
+    assert status == 0
+    check(x, out, 0.1)
+
+
+@pytest.mark.parametrize("tokens", [[2, 3], [40, 90]], ids=["few", "many"])
+def test_out_at_sixteen_bytes(tokens):
+    """out need not be aligned to more than 16 bytes, and nothing around it is written."""
+    x = make(tokens, [200, 130], (8, 2, 64), torch.bfloat16)
+    want, _ = run(x, 0.1)
+    n = want.numel()
+    room = torch.full((n + 8,), 7.0, device="cuda")
+    out = room[4:4 + n].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    got, status = run(x, 0.1, out=out)
+    assert status == 0 and torch.equal(got, want)
+    assert (room[:4] == 7).all() and (room[4 + n:] == 7).all()
+
+
+def test_values_that_differ_by_much():
+    # one state outweighs all others, far into the span; huge and tiny scores beside each other
+    x = make([3, 140], [3000, 500], (8, 2, 64), torch.bfloat16)
+    x["q"] *= 20
+    x["k"][0, 2500] *= 8
+    out, status = run(x, 1.0)
+    assert status == 0
+    check(x, out, 1.0)
+
+
+def test_one_state_is_returned():
+    # The weight is 2^(x - m) with x - m what rounding m left, not exactly 1; it enters the product as
+    # two bf16 parts, 2^-8 * 2^-8 off at most, is divided by itself (2^-23) and multiplied (2^-24).
+    for tokens in ([1, 1], [30, 40]):
+        x = make(tokens, [1, 1], (8, 2, 64), torch.bfloat16)
+        out, _ = run(x, 0.7)
+        for e in range(2):
+            v = x["v"][e, 0].float().repeat_interleave(4, 0).cuda()
+            assert ((out[x["starts"][e]:x["starts"][e + 1]] - v).abs() <= v.abs() * (2.0 ** -16 + 2.0 ** -22)).all()
+
+
+def test_refusals():
+    x = make([2, 3], [100, 90], (8, 2, 64), torch.bfloat16)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = [x["q"].cuda(), x["k"].cuda(), x["v"].cuda(), i32(x["states"]), i32(x["starts"])]
+    for i, bad in [(0, x["q"].cuda().half()), (1, args[1].float()), (2, args[2][:, :50]), (3, i32([1])), (4, i32([0, 2])),
+                   (3, torch.tensor(x["states"], dtype=torch.int32))]:
+        with pytest.raises(ValueError):
+            gqa.cross_attend(*args[:i], bad, *args[i + 1:], 0.1)
+    with pytest.raises(gqa.GQAError):
+        gqa.cross_attend(*args, float("inf"))
+    with pytest.raises(gqa.GQAError):
+        gqa.cross_attend(args[0][:, :7].contiguous(), *args[1:], 0.1)  # 7 heads over 2

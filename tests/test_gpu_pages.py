@@ -327,3 +327,42 @@ def test_captured_step():
         m.lens += 1
     torch.cuda.synchronize()
     m.same(table, lens, refs)
+
+
+def test_refusals():
+    m = Pages(3, 4, 16, 8)
+    table, lens, refs = m.gpu()
+    out, lens_out = torch.empty_like(table), torch.empty_like(lens)
+    with pytest.raises(gqa.GQAError):  # the tables overlap
+        gqa.pages_fork(i32([0, 1, 2]), table, lens, table, lens_out, refs)
+    with pytest.raises(gqa.GQAError):
+        gqa.pages_fork(i32([0, 1, 2]), table, lens, out, lens, refs)
+    with pytest.raises(ValueError):
+        gqa.pages_fork(i32([0, 1]), table, lens, out, lens_out, refs)
+    with pytest.raises(ValueError):
+        gqa.pages_free(i32([0]), table.long(), lens, refs)
+    with pytest.raises(gqa.GQAError):
+        gqa.pages_reserve(table, lens, refs, 0, 8)
+    with pytest.raises(gqa.GQAError):
+        gqa.pages_reserve(table, lens, refs, 1, 8, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(gqa.GQAError):
+        gqa.pages_compact(table, torch.zeros(17, dtype=torch.int32, device="cuda")[1:])  # counts not 16-byte aligned
+    pool = torch.zeros((16, 8, 2, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        gqa.pages_copy(pool, pool[:8], i32([[0, 1]]))
+    with pytest.raises(ValueError):
+        gqa.pages_copy(pool, pool, i32([0, 1]))
+    with pytest.raises(gqa.GQAError):
+        gqa.pages_copy(torch.zeros((4, 8, 2, 96), dtype=torch.bfloat16, device="cuda"),
+                       torch.zeros((4, 8, 2, 96), dtype=torch.bfloat16, device="cuda"), i32([[0, 1]]))
+
+
+def test_copy_far_pages():
+    """Pages whose offsets pass 32 bits (of 16-byte vectors: 2^31 is 32 GiB in; of bytes here)."""
+    n_pages = 140_000  # of 32 KiB: 4.6 GB a pool
+    k = torch.zeros((n_pages, 16, 8, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    k[n_pages - 1] = 3
+    v[n_pages - 2] = 5
+    gqa.pages_copy(k, v, i32([[n_pages - 1, 2], [n_pages - 2, n_pages - 3], [0, 1]]))
+    assert (k[2] == 3).all() and (v[n_pages - 3] == 5).all() and not k[3].any() and not v[2].any()

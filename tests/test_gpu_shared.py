@@ -262,3 +262,75 @@ def test_on_another_stream():
     side = torch.cuda.Stream()
     got, _ = run(x, 0.1, stream=side)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("Q", [1, 32])  # own rows in a launch of their own, and beside the shared ones
+def test_wait_timeout_is_reported_and_the_context_recovers(Q):
+    x = make([0, 17, 20], [1000, 77], [Q + i * 9 for i in range(20)], 20, Q, (32, 4, 128), torch.bfloat16)
+    gqa.set_wait_timeout_ns(1)
+    try:
+        _, status = run(x, 0.1)
+    finally:
+        gqa.set_wait_timeout_ns(0)
+    assert status & gqa.STATUS_WAIT_TIMEOUT
+    out, status = run(x, 0.1)
+    assert status == 0
+    close(out, expect(x, 0.1), tol(x, 0.1))
+
+
+@pytest.mark.parametrize("case", [
+    # enough spans that a thread (and a warp) has several to look at; many empty ones among them
+    (list(range(0, 700)), [(i * 37) % 150 * (i % 3 > 0) for i in range(699)], [(i * 13) % 40 * (i % 5 > 0) for i in range(700)]),
+    ([0] + [3] * 399 + [4], [8] * 400, [i % 7 for i in range(4)]),
+], ids=["many", "empty groups"])
+def test_many_groups(case):
+    starts, prefix, own = case
+    x = make(starts, prefix, own, len(own), 1, (8, 2, 64), torch.bfloat16)
+    out, status = run(x, 0.125)
+    assert status == 0
+    close(out, expect(x, 0.125), tol(x, 0.125))
+
+
+def test_calls_on_two_streams_at_once():
+    x = make([0, 17, 20], [3000, 77], [i * 9 for i in range(20)], 20, 1, (32, 4, 128), torch.bfloat16)
+    y = make([0, 5], [1500], [300] * 5, 5, 1, (8, 2, 64), torch.bfloat16)
+    want = [run(v, 0.1)[0] for v in (x, y)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = []
+    for v in (x, y):
+        c = {n: v[n].cuda() for n in ("q", "k_prefix", "v_prefix", "k_cache", "v_cache")}
+        args.append((c["q"], c["k_prefix"], c["v_prefix"], i32(v["prefix"]), i32(v["starts"]), c["k_cache"], c["v_cache"], i32(v["own"])))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            got[i].append(gqa.decode_shared(*args[i], 0.1, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_refusals():
+    x = make([0, 2], [64], [9, 8], 2, 1, (8, 2, 64), torch.bfloat16)
+    c = {n: x[n].cuda() for n in ("q", "k_prefix", "v_prefix", "k_cache", "v_cache")}
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = [c["q"], c["k_prefix"], c["v_prefix"], i32([64]), i32([0, 2]), c["k_cache"], c["v_cache"], i32([9, 8])]
+
+    def refused(kind, i, value, **kw):
+        with pytest.raises(kind):
+            gqa.decode_shared(*args[:i], value, *args[i + 1:], 0.1, **kw)
+
+    refused(ValueError, 0, c["q"].cpu())
+    refused(ValueError, 0, c["q"].half())
+    refused(ValueError, 0, c["q"].float())                    # the caches are bf16
+    refused(ValueError, 1, c["k_prefix"].transpose(1, 2))     # not dense
+    refused(ValueError, 3, i32([64]).long())
+    refused(ValueError, 4, i32([0, 1, 2]))
+    refused(ValueError, 7, i32([9, 8, 7]))
+    refused(ValueError, 7, args[7], out=torch.empty(2, 8, 64, dtype=torch.bfloat16, device="cuda"))
+    refused(gqa.GQAError, 7, args[7], workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(gqa.GQAError):
+        gqa.decode_shared(*args, float("nan"))
+    with pytest.raises(gqa.GQAError):  # 33 query tokens
+        gqa.decode_shared(c["q"].unsqueeze(1).repeat(1, 33, 1, 1).contiguous(), *args[1:], 0.1)
