@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(256, 3) span_merge_shared_kernel(const __grid_
         if (p1.own_after) so.row0 = max(sg.rows, 0);
         if (tok < sg.tok0 || tok >= sg.tok0 + sg.ntok) sg.rows = 0;  // a group whose start is out of range
     }
-    valid = valid && n >= so.row0 && n <= p1.own_max && (p1.Q == 1 || n - so.row0 >= p1.Q);  // own_rows_of
+    // as own_rows_of; an empty sequence of a paged cache attends nothing, shared rows neither
+    valid = valid && !(p1.own_after && n == 0) && n >= so.row0 && n <= p1.own_max && (p1.Q == 1 || n - so.row0 >= p1.Q);
     so.rows = n - so.row0;
     Join<D> j;
     if (valid && sg.rows > 0) add_span<D>(p0, g, sg, tok, kvh, h, row, false, sub, part, parts, j);

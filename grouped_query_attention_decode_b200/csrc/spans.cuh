@@ -85,6 +85,7 @@ __device__ __forceinline__ bool own_rows_of(const SpanParams &p, int b, int &row
     const int n = __ldg(p.lens + b);
     row0 = rows = 0;
     if (p.own_after) {
+        if (n == 0 && p.Q == 1) return true;  // an empty sequence attends nothing, shared rows neither
         const int g = group_of(p, b);
         if (g >= 0) row0 = shared_rows_of(p, g);
         if (row0 < 0) return row0 = 0, false;

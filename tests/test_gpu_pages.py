@@ -249,8 +249,9 @@ def test_samples_of_two_prompts(dtype):
     table = torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
     lens, refs, status = i32([0] * B), i32([0] * n_pages), word()
     rows = [([], []) for _ in range(B)]  # what each sequence has appended, on the host
+    live = list(range(B))
 
-    def step(live):
+    def step():
         gqa.pages_copy(k_pool, v_pool, gqa.pages_reserve(table, lens, refs, 1, ps, status=status))
         kn, vn = normal((B, H_kv, d), g, dtype), normal((B, H_kv, d), g, dtype)
         gqa.kv_append_paged(kn.cuda(), vn.cuda(), k_pool, v_pool, table, lens, status=status)
@@ -259,7 +260,7 @@ def test_samples_of_two_prompts(dtype):
             rows[b][1].append(vn[b])
 
     for _ in range(70):
-        step(range(B))
+        step()
     # samples 0..5 of prompt 0, 6..8 of prompt 1 (which is sequence 3)
     parents = [0] * 6 + [3] * 3
     table2, lens2 = torch.empty_like(table), torch.empty_like(lens)
@@ -267,28 +268,19 @@ def test_samples_of_two_prompts(dtype):
     table, lens = table2, lens2
     rows = [(list(rows[p][0]), list(rows[p][1])) for p in parents]
     starts, shared = i32([0, 6, 9]), i32([64, 64])
-    live = list(range(B))
     for t in range(20):
-        step(live)
-        if t == 10:
+        step()
+        if t >= 10:  # two samples have ended; they still take part in every append
             gqa.pages_free(i32([1, 4]), table, lens, refs, status=status)
-            rows[1], rows[4] = ([], []), ([], [])
             live = [b for b in live if b not in (1, 4)]
-            gqa.pages_reserve(table, lens, refs, 1, ps, status=status)
+        if t == 10:
             pairs, n = gqa.pages_compact(table, refs, status=status)
             gqa.pages_copy(k_pool, v_pool, pairs)
             used = torch.unique(table[table >= 0])
             assert int(n) == len(used) and int(used.max()) == int(n) - 1
         if t % 5 == 1:
             q = normal((B, H_q, d), g, dtype)
-            # empty sequences hold no shared rows: groups of those that do
-            if t < 10:
-                out = gqa.decode_shared_paged(q.cuda(), k_pool, v_pool, table, lens, starts, shared, 0.2, status=status)
-            else:
-                pick = torch.tensor(live, device="cuda")
-                out = torch.zeros((B, H_q, d), device="cuda")
-                out[pick] = gqa.decode_shared_paged(q.cuda()[pick], k_pool, v_pool, table[pick].contiguous(), lens[pick].contiguous(),
-                                                    i32([0, 4, 7]), shared, 0.2, status=status)
+            out = gqa.decode_shared_paged(q.cuda(), k_pool, v_pool, table, lens, starts, shared, 0.2, status=status)
             whole = gqa.decode_paged(q.cuda(), k_pool, v_pool, table, lens, 0.2, status=status)
             for b in live:
                 k, v = torch.stack(rows[b][0]).cuda(), torch.stack(rows[b][1]).cuda()

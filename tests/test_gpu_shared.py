@@ -212,6 +212,22 @@ def test_shared_rows_must_be_whole_pages():
         assert int(status.item()) == gqa.STATUS_SEQLEN_RANGE and not out.any()
 
 
+def test_empty_sequences_of_a_group():
+    # sequences that have been freed stay in their group: zeros, and no complaint
+    x = make([0, 4], [512], [40, 1, 300, 77], 4, 1, (64, 8, 128), torch.bfloat16)
+    kp, vp, table, lens = (t.cuda() for t in paged(x, 16))
+    args = (x["q"].cuda(), kp, vp, table, lens, torch.tensor([0, 4], dtype=torch.int32, device="cuda"),
+            torch.tensor([512], dtype=torch.int32, device="cuda"), 0.1)
+    whole = gqa.decode_shared_paged(*args)
+    lens[2] = 0
+    table[2] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = gqa.decode_shared_paged(*args, status=status)
+    assert int(status) == 0 and not out[2].any()
+    bound = tol(x, 0.1)  # the line of tiles is cut elsewhere
+    assert float((out[[0, 1, 3]] - whole[[0, 1, 3]]).abs().max()) <= 2 * bound
+
+
 def test_bad_page_is_reported():
     x = make([0, 2], [64], [9, 8], 2, 1, (8, 2, 64), torch.bfloat16)
     kp, vp, table, lens = (t.cuda() for t in paged(x, 16))
