@@ -605,10 +605,12 @@ bool span_plan(SpanPlan &s, int P, int N, int B, int Q, int H_q, int H_kv, int d
     const size_t rows = B > 0 ? 2ull * N * H_q : 0;
     s.res_ml = s.res + up(rows * d * 4);
     s.bytes = s.res_ml + up(rows * 8);
-    // With few query rows per span -- up to 16, on average over the encoder sequences -- a product
-    // of 128 of them is mostly padding and its chain of waits what is paid for.
+    // With few query rows per span -- up to 32, on average over the encoder sequences; 17 to 32 of them
+    // read the span twice -- a product of 128 of them is mostly padding and its chain of waits what is
+    // paid for.  64 encoder sequences of 600 states, 24 rows: 35 us, in span_tc.cu 52; 32 of 500 under 64
+    // heads, 32 rows: 111 and 145; 16 of 1200, 32 rows: 26 and 26; 4 of 4000 (d = 128), 32 rows: 33 and 30.
     const long long few_tokens = B > 0 ? Q : (static_cast<long long>(N) + P - 1) / P;
-    s.few = tc && few_tokens * s.r <= kFewRows;
+    s.few = tc && few_tokens * s.r <= 2 * kFewRows && s.r <= kFewRows;
     if (s.few) {
         s.few_rb = s.r;
         s.few_workers = sms * span_few_warps(d);
