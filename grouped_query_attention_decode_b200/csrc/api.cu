@@ -610,10 +610,13 @@ bool span_plan(SpanPlan &s, int P, int N, int B, int Q, int H_q, int H_kv, int d
     // paid for.  64 encoder sequences of 600 states, 24 rows: 35 us, in span_tc.cu 52; 32 of 500 under 64
     // heads, 32 rows: 111 and 145; 16 of 1200, 32 rows: 26 and 26; 4 of 4000 (d = 128), 32 rows: 33 and 30.
     const long long few_tokens = B > 0 ? Q : (static_cast<long long>(N) + P - 1) / P;
-    s.few = tc && few_tokens * s.r <= 2 * kFewRows && s.r <= kFewRows;
+    // float32: units of 16 rows in span_f32.cu for up to 16 rows.  16 sequences of 4000 rows, 4 query
+    // rows: 130 us, in units of 64 rows 292; 64 of 600, 12 rows (d = 64): 90 and 123, 16 rows: 110 and
+    // 124, 32 rows: 204 and 135.
+    s.few = few_tokens * s.r <= (tc ? 2 * kFewRows : kFewRows) && s.r <= kFewRows;
     if (s.few) {
         s.few_rb = s.r;
-        s.few_workers = sms * span_few_warps(d);
+        s.few_workers = sms * (tc ? span_few_warps(d) : 2);
         const int blk = kFewRows / s.r;
         s.few_u1 = static_cast<long long>(N) / blk + P + 1;
         const size_t at = B > 0 ? s.bytes : 0;
@@ -719,41 +722,48 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
     p.res = reinterpret_cast<float *>(w + s.res);
     p.res_ml = reinterpret_cast<float *>(w + s.res_ml);
 
-    if (!tc) {
-        const int res = launch_span_f32(p, static_cast<const float *>(a.q), static_cast<const float *>(a.k_shared),
-                                        static_cast<const float *>(a.v_shared), static_cast<const float *>(a.k_own),
-                                        static_cast<const float *>(a.v_own), stream);
-        return res != GQA_OK ? res : launch_span_merge(p, p, stream);
-    }
-    if (encode_fn() == nullptr) return GQA_ERR_CUDA;
-    // caches as (d, H_kv, rows, prefixes or sequences) or (d, H_kv, page_size, n_pages)
-    const int rows_g = paged ? a.page_size : a.g_max, rows_o = paged ? a.page_size : a.own_max;
-    const int outer_g = paged ? a.n_pages : a.P, outer_o = paged ? a.n_pages : a.B;
-    const int box = paged && a.page_size < s.T ? a.page_size : s.T;
     SpanParams fp = p;
-    CUtensorMap few_k, few_v;
     if (s.few) {
         fp.rb = s.few_rb;
         fp.HB = 1;
         fp.tb = fp.blk = kFewRows / s.few_rb;
         fp.nblkQ = (a.Q + fp.blk - 1) / fp.blk;
-        fp.T = fp.RT = fp.unit_rows = kFewRows;
+        fp.T = tc ? 16 : 64;
+        fp.RT = fp.unit_rows = kFewRows;
         fp.G = s.few_workers;
         fp.u1 = 0;
         fp.rec = reinterpret_cast<SpanRecord *>(w + s.few_rec);
         fp.uinfo = reinterpret_cast<int4 *>(w + s.few_uinfo);
         fp.slots = reinterpret_cast<float *>(w + s.few_slots);
         fp.slot_floats = kFewRows * (a.d + 2);
+        if (a.B > 0) {
+            p.s_end = fp.s_begin = a.P;
+            fp.behind_shared = 1;
+        }
+    }
+    const bool all_few = s.few && a.B == 0;  // the only launch
+    if (!tc) {
+        const float *q = static_cast<const float *>(a.q), *ks = static_cast<const float *>(a.k_shared), *vs = static_cast<const float *>(a.v_shared);
+        const float *ko = static_cast<const float *>(a.k_own), *vo = static_cast<const float *>(a.v_own);
+        int res = all_few ? GQA_OK : launch_span_f32(p, q, ks, vs, ko, vo, stream);
+        if (res == GQA_OK && s.few) res = launch_span_f32(fp, q, ks, vs, ko, vo, stream);
+        return res != GQA_OK ? res : launch_span_merge(all_few ? fp : p, fp, stream);
+    }
+    if (encode_fn() == nullptr) return GQA_ERR_CUDA;
+    // caches as (d, H_kv, rows, prefixes or sequences) or (d, H_kv, page_size, n_pages)
+    const int rows_g = paged ? a.page_size : a.g_max, rows_o = paged ? a.page_size : a.own_max;
+    const int outer_g = paged ? a.n_pages : a.P, outer_o = paged ? a.n_pages : a.B;
+    const int box = paged && a.page_size < s.T ? a.page_size : s.T;
+    CUtensorMap few_k, few_v;
+    if (s.few) {
         const bool own = a.B > 0;
         if (!encode_cache_map(&few_k, own ? a.k_own : a.k_shared, own ? outer_o : outer_g, a.H_kv, a.d, own ? rows_o : rows_g, 8) ||
             !encode_cache_map(&few_v, own ? a.v_own : a.v_shared, own ? outer_o : outer_g, a.H_kv, a.d, own ? rows_o : rows_g, 8))
             return GQA_ERR_SHAPE;
-        if (!own) {
-            const int rc2 = launch_span_few(fp, few_k, few_v, a.q, stream);
-            return rc2 != GQA_OK ? rc2 : launch_span_merge(fp, fp, stream);
-        }
-        p.s_end = fp.s_begin = a.P;
-        fp.behind_shared = 1;
+    }
+    if (all_few) {
+        const int res = launch_span_few(fp, few_k, few_v, a.q, stream);
+        return res != GQA_OK ? res : launch_span_merge(fp, fp, stream);
     }
     SpanMaps m;
     if (!encode_q_map(&m.q_shared, a.q, a.N, s.tb, a.H_q, a.d, s.rb) ||

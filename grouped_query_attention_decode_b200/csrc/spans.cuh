@@ -53,7 +53,7 @@ struct SpanParams {
     float *slots;          // [2 * G][slot_floats]
     long long slot_floats;
     float *res, *res_ml;   // [2][N * H_q][d] sums and [2][N * H_q][2] (m, l) of whole units
-    int behind_shared;     // span_few.cu: launched behind the launch over the shared spans
+    int behind_shared;     // few rows: launched behind the launch over the shared spans (span_few.cu)
     int u1;                // number of the own spans' first token block, after the shared spans'
     int unit_rows;         // query rows of a slot
 };
