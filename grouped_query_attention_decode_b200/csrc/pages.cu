@@ -443,7 +443,8 @@ extern "C" int gqa_pages_fork(const int32_t *parents, const int32_t *table_in, c
                               int32_t *table_out, int32_t *lens_out, int B_out, int max_pages, int32_t *ref_counts,
                               int n_pages, int32_t *status, cudaStream_t stream) {
     if (!parents || !table_in || !lens_in || !table_out || !lens_out || !ref_counts) return GQA_ERR_NULL;
-    if (!table_fits(B_in, max_pages) || !table_fits(B_out, max_pages) || n_pages <= 0) return GQA_ERR_SHAPE;
+    if (!table_fits(B_in, max_pages) || !table_fits(B_out, max_pages) || n_pages <= 0 || static_cast<long long>(B_in) + B_out > (1ll << 30))
+        return GQA_ERR_SHAPE;
     for (const int32_t *p : {parents, table_in, lens_in, static_cast<const int32_t *>(table_out), static_cast<const int32_t *>(lens_out),
                              static_cast<const int32_t *>(ref_counts), static_cast<const int32_t *>(status)})
         if (!aligned(p, 4)) return GQA_ERR_ALIGNMENT;

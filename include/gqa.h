@@ -314,14 +314,18 @@ int gqa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
  *   group g hold their first shared_rows[g] rows in the same pages (as gqa_pages_fork leaves
  *   them).  Those rows are read through the table of the group's first sequence, which has to hold
  *   them.  shared_rows[g] must be a multiple of page_size and at most seq_lens[b] (- Q for Q > 1) of
- *   every sequence of the group; an empty sequence (seq_lens[b] = 0, Q = 1) gets zeros.  page_size must be a multiple of 8 and divide 128 or be a multiple of 128 (any
- *   multiple of 8 for float32).
+ *   every sequence of the group; an empty sequence (seq_lens[b] = 0, Q = 1) gets zeros.
+ *   page_size must be a multiple of 8 and divide 128 or be a multiple of 128 (any multiple of 8
+ *   for float32).
  * A length out of range -- negative, past its capacity, own rows < Q (Q > 1), shared rows that do
  * not fit the rules above -- gives out[b] = 0 for the sequences concerned and sets
- * GQA_STATUS_SEQLEN_RANGE.  bfloat16 (tensor cores) and float32 (CUDA cores).  P >= 1, d, heads and
- * alignment as for gqa_decode.  The workspace needs gqa_decode_shared_workspace_size() bytes and
- * no zero-fill; two calls that may run at the same time must not share one.  Launches two kernels
- * on `stream`.
+ * GQA_STATUS_SEQLEN_RANGE.  Cached rows that no token of a sequence sees are never read into a
+ * result; a drafted token's row that is not finite can make the outputs of the sequence's other
+ * drafts NaN, those before it included.  bfloat16 (tensor cores) and float32 (CUDA cores).  P >= 1;
+ * d, heads and alignment as for gqa_decode.  The workspace needs
+ * gqa_decode_shared_workspace_size() bytes and no zero-fill; two calls that may run at the same
+ * time must not share one.  Launches two kernels on `stream`, three when a sequence has at most 32
+ * query rows (16 for float32) per key/value head: the shared rows, the own rows, and what joins them.
  */
 size_t gqa_decode_shared_workspace_size(int B, int Q, int P, int H_q, int H_kv, int d,
                                         gqa_dtype_t dtype);
@@ -353,7 +357,8 @@ int gqa_decode_shared_paged(const void *q, const void *k_pool, const void *v_poo
  *            otherwise, and that sequence's tokens are not written).  Tokens before q_start[0] and
  *            from q_start[E] on are neither read nor written.
  * Types, d, heads, alignment and errors as gqa_decode; the workspace needs
- * gqa_cross_attend_workspace_size() bytes and no zero-fill.  Launches two kernels on `stream`.
+ * gqa_cross_attend_workspace_size() bytes and no zero-fill; two calls that may run at the same
+ * time must not share one.  Launches two kernels on `stream`.
  */
 size_t gqa_cross_attend_workspace_size(int E, int N, int H_q, int H_kv, int d, gqa_dtype_t dtype);
 int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const int32_t *enc_lens,
@@ -391,8 +396,8 @@ int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const 
  *   (-1, -1): run gqa_pages_copy on it before appending.  The lengths do not change.  A sequence
  *   whose rows do not fit max_pages * page_size gets nothing (GQA_STATUS_APPEND_OVERFLOW).  When
  *   free pages run out, the first sequence that they do not suffice for and those behind it that
- *   need any get none (GQA_STATUS_POOL_FULL); appending to such a sequence would write a shared
- *   page, so check the status, or the counts, before.
+ *   need any get none (GQA_STATUS_POOL_FULL), and rows about to be written may still lie in shared
+ *   pages: append to no sequence then, but free pages and call again.
  * gqa_pages_compact: moves the pages in use to the front of the pool.  With n of them, the pages
  *   numbered n and up, in ascending order, take the places of the free ones below n; tables and
  *   counts follow, copies [max(1, n_pages / 2)][2] gets the moves, (-1, -1) behind the last, and

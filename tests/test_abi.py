@@ -184,6 +184,7 @@ def test_pages_host_checks(lib):
         return lib.gqa_pages_fork(parents, tin, lin, bi, tout, lout, bo, mp, refs, n, None, None)
     assert fork(parents=None) == -1 and fork(refs=None) == -1
     assert fork(bi=0) == -2 and fork(bo=0) == -2 and fork(mp=0) == -2 and fork(n=0) == -2
+    assert fork(bi=1 << 30, bo=1 << 30, mp=1) == -2
     assert fork(tin=P(0x100002)) == -6
     assert fork(tout=P(0x100000 + 4 * 7)) == -11 and fork(lout=P(0x300004)) == -11
     assert lib.gqa_pages_free(None, 1, T0, L0, 2, 4, A16, 8, None, None) == -1

@@ -75,8 +75,9 @@ def test_tokens_outside_are_left():
     assert (out[:2] == 7).all() and (out[7:] == 7).all() and not out[4:7].any()
 
 
-def test_out_of_range_is_reported():
-    x = make([2, 3, 2], [100, 90, 80], (8, 2, 64), torch.bfloat16)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_out_of_range_is_reported(dtype):
+    x = make([2, 3, 2], [100, 90, 80], (8, 2, 64), dtype)
     good, _ = run(x, 0.1)
     for bad in (-1, 1000):
         out, status = run(dict(x, states=[100, bad, 80]), 0.1)
@@ -87,8 +88,9 @@ def test_out_of_range_is_reported():
     assert torch.equal(out[:5], good[:5]) and (out[5:] == 7).all()
 
 
-def test_captured_and_replayed():
-    x = make([5, 70], [400, 333], (64, 8, 128), torch.bfloat16)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_captured_and_replayed(dtype):
+    x = make([5, 70], [400, 333], (64, 8, 128), dtype)
     want, _ = run(x, 0.1)
     q, k, v = x["q"].cuda(), x["k"].cuda(), x["v"].cuda()
     states = torch.tensor(x["states"], dtype=torch.int32, device="cuda")
@@ -122,20 +124,22 @@ def test_far_rows():
         assert float((out[i].double() - attend64(q[i], k[-1], v[-1], 0.3)).abs().max()) <= bound
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("heads", [(8, 8, 64), (8, 2, 64), (64, 2, 128), (12, 4, 128), (24, 1, 64)], ids=lambda h: "%d_%d_%d" % h)
 @pytest.mark.parametrize("tokens", [[1, 1, 1], [2, 0, 1, 3], [1, 0, 0, 0, 0, 0, 0, 40], [4] * 9], ids=str)
-def test_few_tokens(tokens, heads):
+def test_few_tokens(tokens, heads, dtype):
     """One token, a beam or two per encoder sequence, and one sequence with many more than the mean."""
     states = [(i * 211) % 700 for i in range(len(tokens))]  # the first has none
-    x = make(tokens, states, heads, torch.bfloat16, before=1, behind=2)
+    x = make(tokens, states, heads, dtype, before=1, behind=2)
     out, status = run(x, 0.1, out=torch.full(x["q"].shape, 7.0, device="cuda"))
     assert status == 0
     check(x, out, 0.1)
     assert (out[0] == 7).all() and (out[-2:] == 7).all()
 
 
-def test_few_tokens_out_of_range():
-    x = make([1, 1, 1], [100, 90, 80], (8, 8, 64), torch.bfloat16)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_few_tokens_out_of_range(dtype):
+    x = make([1, 1, 1], [100, 90, 80], (8, 8, 64), dtype)
     good, _ = run(x, 0.1)
     out, status = run(dict(x, states=[100, -1, 80]), 0.1)
     assert status == gqa.STATUS_SEQLEN_RANGE and torch.equal(out[::2], good[::2]) and not out[1].any()
@@ -144,10 +148,11 @@ def test_few_tokens_out_of_range():
     assert status == gqa.STATUS_GROUP_RANGE
 
 
-def test_few_tokens_repeat():
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_few_tokens_repeat(dtype):
     # the workspace's counters are set anew by each call
-    x = make([1] * 5, [700, 3, 2000, 129, 0], (16, 4, 128), torch.bfloat16)
-    ws = torch.full((gqa.cross_workspace_size(5, 5, 16, 4, 128, torch.bfloat16),), 255, dtype=torch.uint8, device="cuda")
+    x = make([1] * 5, [700, 3, 2000, 129, 0], (16, 4, 128), dtype)
+    ws = torch.full((gqa.cross_workspace_size(5, 5, 16, 4, 128, dtype),), 255, dtype=torch.uint8, device="cuda")
     first, _ = run(x, 0.1, workspace=ws)
     again, _ = run(x, 0.1, workspace=ws)
     assert torch.equal(first, again)

@@ -185,8 +185,9 @@ def test_same_as_decode_paged():
     assert float((out - whole).abs().max()) <= 2 * tol(x, 0.09)
 
 
-def test_lengths_out_of_range_are_reported():
-    x = make([0, 2, 4], [64, 64], [9, 8, 7, 6, 5], 5, 1, (8, 2, 64), torch.bfloat16)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_lengths_out_of_range_are_reported(dtype):
+    x = make([0, 2, 4], [64, 64], [9, 8, 7, 6, 5], 5, 1, (8, 2, 64), dtype)
     good, _ = run(x, 0.1)
     y = dict(x, own=[9, -1, 7, 1000, 5])
     out, status = run(y, 0.1)
@@ -228,8 +229,9 @@ def test_empty_sequences_of_a_group():
     assert float((out[[0, 1, 3]] - whole[[0, 1, 3]]).abs().max()) <= 2 * bound
 
 
-def test_bad_page_is_reported():
-    x = make([0, 2], [64], [9, 8], 2, 1, (8, 2, 64), torch.bfloat16)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_bad_page_is_reported(dtype):
+    x = make([0, 2], [64], [9, 8], 2, 1, (8, 2, 64), dtype)
     kp, vp, table, lens = (t.cuda() for t in paged(x, 16))
     table[1, 4] = 10_000
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -239,19 +241,21 @@ def test_bad_page_is_reported():
     assert float((out[0].double() - expect(x, 0.1)[0]).abs().max()) <= tol(x, 0.1)
 
 
-def test_repeats_and_workspace_reuse():
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_repeats_and_workspace_reuse(dtype):
     # the same bits again, with a workspace that another call with other sizes has used
-    x = make([0, 17, 20], [1000, 77], [i * 9 for i in range(20)], 20, 1, (32, 4, 128), torch.bfloat16)
-    ws = torch.full((gqa.shared_workspace_size(20, 1, 2, 32, 4, 128, torch.bfloat16) + 4096,), 255, dtype=torch.uint8, device="cuda")
+    x = make([0, 17, 20], [1000, 77], [i * 9 for i in range(20)], 20, 1, (32, 4, 128), dtype)
+    ws = torch.full((gqa.shared_workspace_size(20, 1, 2, 32, 4, 128, dtype) + 4096,), 255, dtype=torch.uint8, device="cuda")
     first, _ = run(x, 0.1, workspace=ws)
-    run(make([0, 1], [40], [3, 2], 2, 1, (8, 2, 64), torch.bfloat16), 0.1, workspace=ws)
+    run(make([0, 1], [40], [3, 2], 2, 1, (8, 2, 64), dtype), 0.1, workspace=ws)
     again, _ = run(x, 0.1, workspace=ws)
     assert torch.equal(first, again)
     close(first, expect(x, 0.1), tol(x, 0.1))
 
 
-def test_captured_and_replayed():
-    x = make([0, 3], [500], [40, 1, 130], 3, 1, (64, 8, 128), torch.bfloat16)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_captured_and_replayed(dtype):
+    x = make([0, 3], [500], [40, 1, 130], 3, 1, (64, 8, 128), dtype)
     c = {n: x[n].cuda() for n in ("q", "k_prefix", "v_prefix", "k_cache", "v_cache")}
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
     prefix, starts, own = i32(x["prefix"]), i32(x["starts"]), i32(x["own"])
