@@ -576,6 +576,7 @@ struct SpanPlan {
     // The launch for few query rows a span (span_few.cu): the own rows of sequences with few of
     // them, or all of a cross attention of few tokens per sequence.
     bool few = false;
+    bool few_all = false;  // the few-row launch takes every span
     int few_rb, few_workers;
     long long few_u1;
     size_t few_rec, few_uinfo, few_slots;
@@ -618,9 +619,14 @@ bool span_plan(SpanPlan &s, int P, int N, int B, int Q, int H_q, int H_kv, int d
         s.few_rb = s.r;
         s.few_workers = sms * (tc ? span_few_warps(d) : 2);
         const int blk = kFewRows / s.r;
-        s.few_u1 = static_cast<long long>(N) / blk + P + 1;
+        // The same launch takes the shared rows when the groups have as few query rows on average.  bf16,
+        // 32/8 heads, d = 128, prompts of 2000 rows and 300 own ones: 8 prompts of 2 sequences (8 rows) 25 us,
+        // by two launches 43; 4 of 8 (32 rows) 29 and 40; 16 prompts of 4 (64/8 heads, 32 rows) 58 and 57, of
+        // 12 (48 rows) 93 and 72.  float32, 4 samples of 192 rows (16): 11.8 and 14.8.
+        s.few_all = B == 0 || (static_cast<long long>(N) + P - 1) / P * s.r <= (tc ? 2 * kFewRows : kFewRows);
+        s.few_u1 = s.few_all ? static_cast<long long>(N) / blk + P + 1 : 0;
         const size_t at = B > 0 ? s.bytes : 0;
-        const long long units = (B > 0 ? static_cast<long long>(B) * ((Q + blk - 1) / blk) : s.few_u1) * H_kv;
+        const long long units = (s.few_u1 + static_cast<long long>(B) * ((Q + blk - 1) / blk)) * H_kv;
         if (units > (1ll << 30)) return false;
         s.few_rec = at;
         s.few_uinfo = s.few_rec + up(static_cast<size_t>(s.few_workers) * sizeof(SpanRecord));
@@ -731,17 +737,25 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
         fp.T = tc ? 16 : 64;
         fp.RT = fp.unit_rows = kFewRows;
         fp.G = s.few_workers;
-        fp.u1 = 0;
+        fp.u1 = static_cast<int>(s.few_u1);
         fp.rec = reinterpret_cast<SpanRecord *>(w + s.few_rec);
         fp.uinfo = reinterpret_cast<int4 *>(w + s.few_uinfo);
         fp.slots = reinterpret_cast<float *>(w + s.few_slots);
         fp.slot_floats = kFewRows * (a.d + 2);
-        if (a.B > 0) {
+        if (!s.few_all) {
             p.s_end = fp.s_begin = a.P;
             fp.behind_shared = 1;
         }
     }
-    const bool all_few = s.few && a.B == 0;  // the only launch
+    const bool all_few = s.few && s.few_all;  // the only launch
+    if (a.B == 0) {
+        // As many workers as 8 to a unit, were all encoder sequences alike: a unit's pieces are joined by all
+        // of them.  One token of 64/8 heads (d = 128) over 100000 states, 148 pieces a row: the call takes
+        // 78 us, by the first one's warps alone 122; with 2 pieces a row of 8 x 509 tokens 196 and 189.
+        SpanParams &last = all_few ? fp : p;
+        const long long tokens = (static_cast<long long>(a.N) + a.P - 1) / a.P;
+        last.spread = last.G >= 8 * static_cast<long long>(a.P) * a.H_kv * last.HB * ((tokens + last.blk - 1) / last.blk);
+    }
     if (!tc) {
         const float *q = static_cast<const float *>(a.q), *ks = static_cast<const float *>(a.k_shared), *vs = static_cast<const float *>(a.v_shared);
         const float *ko = static_cast<const float *>(a.k_own), *vo = static_cast<const float *>(a.v_own);
@@ -754,15 +768,15 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
     const int rows_g = paged ? a.page_size : a.g_max, rows_o = paged ? a.page_size : a.own_max;
     const int outer_g = paged ? a.n_pages : a.P, outer_o = paged ? a.n_pages : a.B;
     const int box = paged && a.page_size < s.T ? a.page_size : s.T;
-    CUtensorMap few_k, few_v;
-    if (s.few) {
-        const bool own = a.B > 0;
-        if (!encode_cache_map(&few_k, own ? a.k_own : a.k_shared, own ? outer_o : outer_g, a.H_kv, a.d, own ? rows_o : rows_g, 8) ||
-            !encode_cache_map(&few_v, own ? a.v_own : a.v_shared, own ? outer_o : outer_g, a.H_kv, a.d, own ? rows_o : rows_g, 8))
-            return GQA_ERR_SHAPE;
-    }
+    SpanFewMaps few;
+    if (all_few && (!encode_cache_map(&few.kv[0], a.k_shared, outer_g, a.H_kv, a.d, rows_g, 8) ||
+                    !encode_cache_map(&few.kv[1], a.v_shared, outer_g, a.H_kv, a.d, rows_g, 8)))
+        return GQA_ERR_SHAPE;
+    if (s.few && a.B > 0 && (!encode_cache_map(&few.kv[2], a.k_own, outer_o, a.H_kv, a.d, rows_o, 8) ||
+                             !encode_cache_map(&few.kv[3], a.v_own, outer_o, a.H_kv, a.d, rows_o, 8)))
+        return GQA_ERR_SHAPE;
     if (all_few) {
-        const int res = launch_span_few(fp, few_k, few_v, a.q, stream);
+        const int res = launch_span_few(fp, few, a.q, stream);
         return res != GQA_OK ? res : launch_span_merge(fp, fp, stream);
     }
     SpanMaps m;
@@ -786,7 +800,7 @@ int span_impl(const SpanArgs &a, float scale, gqa_dtype_t dtype, float *out, voi
          !encode_cache_map(&m.v_own8, a.v_own, outer_o, a.H_kv, a.d, rows_o, 8)))
         return GQA_ERR_SHAPE;
     int res = launch_span_tc(m, p, stream);
-    if (res == GQA_OK && s.few) res = launch_span_few(fp, few_k, few_v, a.q, stream);
+    if (res == GQA_OK && s.few) res = launch_span_few(fp, few, a.q, stream);
     return res != GQA_OK ? res : launch_span_merge(p, fp, stream);
 }
 

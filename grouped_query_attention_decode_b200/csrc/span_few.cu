@@ -13,6 +13,10 @@
 // and results are in the registers of the one warp that needs them, costs nothing against tcgen05
 // and saves its round trips through tensor memory.  P enters as two bf16 parts (the outputs are
 // float32), each tile's P.V starts from zero and is added in fp32, rounded to nearest.
+//
+// Measured (one B200): 32 sequences of 1024 states, 64/64 heads, d = 64, one token each: 537 MB in
+// 110 us, 4.9 TB/s; issue slots are 42 % used, the tensor pipe 26 %, and a warp mostly waits for its
+// own chain.  Short calls also pay ~6 us before the first copy.
 #include <cstdint>
 
 #include "device.cuh"
@@ -63,7 +67,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(FewCfg<D>::WARPS * 32, 1)
-span_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+span_few_kernel(const __grid_constant__ SpanFewMaps maps,
                 const __nv_bfloat16 *__restrict__ q, const __grid_constant__ SpanParams p) {
     using C = FewCfg<D>;
     constexpr int T = C::T, S = C::S, KB = C::KB;
@@ -82,8 +86,14 @@ span_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         fence_mbarrier_init();
     }
     if (threadIdx.x == 0) {
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
+        if (p.s_begin < p.P) {
+            prefetch_tmap(maps.kv);
+            prefetch_tmap(maps.kv + 1);
+        }
+        if (p.s_end > p.P) {
+            prefetch_tmap(maps.kv + 2);
+            prefetch_tmap(maps.kv + 3);
+        }
     }
 
     // Behind the launch over the shared rows nothing here depends on it: what that launch waited for
@@ -134,7 +144,9 @@ span_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 if (p.status != nullptr) atomicOr(p.status, GQA_STATUS_PAGE_RANGE);
                 outer = 0;
             }
-            tma_load_4d(to + st * (2 * C::TILE), is_v ? &tm_v : &tm_k, full + st, cb * 64, cg.kvh, row, outer, once);
+            // K and V of the shared rows, then of the own ones
+            const CUtensorMap *tm = maps.kv + (cg.s < p.P ? 0 : 2) + is_v;
+            tma_load_4d(to + st * (2 * C::TILE), tm, full + st, cb * 64, cg.kvh, row, outer, once);
         }
         ++n_copied;
         if (++cj == cg.len) {
@@ -304,7 +316,7 @@ span_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 namespace {
 
 template <int D, bool PAGED>
-int launch_span_few_impl(const SpanParams &p, const CUtensorMap &k, const CUtensorMap &v, const void *q, cudaStream_t stream) {
+int launch_span_few_impl(const SpanParams &p, const SpanFewMaps &maps, const void *q, cudaStream_t stream) {
     using C = FewCfg<D>;
     auto kern = span_few_kernel<D, PAGED>;
     static bool attr_set[64] = {};
@@ -325,7 +337,7 @@ int launch_span_few_impl(const SpanParams &p, const CUtensorMap &k, const CUtens
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, k, v, static_cast<const __nv_bfloat16 *>(q), p) != cudaSuccess) return GQA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, maps, static_cast<const __nv_bfloat16 *>(q), p) != cudaSuccess) return GQA_ERR_CUDA;
     return GQA_OK;
 }
 
@@ -333,10 +345,10 @@ int launch_span_few_impl(const SpanParams &p, const CUtensorMap &k, const CUtens
 
 int span_few_warps(int d) { return d == 128 ? FewCfg<128>::WARPS : FewCfg<64>::WARPS; }
 
-int launch_span_few(const SpanParams &p, const CUtensorMap &k, const CUtensorMap &v, const void *q, cudaStream_t stream) {
+int launch_span_few(const SpanParams &p, const SpanFewMaps &maps, const void *q, cudaStream_t stream) {
     if (p.block_table != nullptr)
-        return p.d == 128 ? launch_span_few_impl<128, true>(p, k, v, q, stream) : launch_span_few_impl<64, true>(p, k, v, q, stream);
-    return p.d == 128 ? launch_span_few_impl<128, false>(p, k, v, q, stream) : launch_span_few_impl<64, false>(p, k, v, q, stream);
+        return p.d == 128 ? launch_span_few_impl<128, true>(p, maps, q, stream) : launch_span_few_impl<64, true>(p, maps, q, stream);
+    return p.d == 128 ? launch_span_few_impl<128, false>(p, maps, q, stream) : launch_span_few_impl<64, false>(p, maps, q, stream);
 }
 
 }  // namespace gqa

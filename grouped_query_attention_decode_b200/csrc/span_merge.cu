@@ -41,6 +41,46 @@ struct Join {
     }
 };
 
+// Threads of a row: eight for each of `parts` shares of its pieces, 1, 4 (a warp) or 16 (a team of
+// four warps).  The sum of the shares, in the first eight threads.
+constexpr int kTeam = 128;
+template <int D>
+struct TeamSums {
+    float2 ml[256 / kTeam][3][8];
+    float4 o[256 / kTeam][3][8][D / 32];
+};
+__device__ __forceinline__ void team_sync() {
+    if (threadIdx.x < kTeam) asm volatile("bar.sync 1, 128;" ::: "memory");
+    else asm volatile("bar.sync 2, 128;" ::: "memory");
+}
+template <int D>
+__device__ __forceinline__ void join_parts(Join<D> &j, int parts, TeamSums<D> &sums) {
+    constexpr int NV = D / 32;
+    if (parts == 1) return;
+#pragma unroll 1
+    for (int x = 8; x <= 16; x <<= 1) {
+        float4 o[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            o[k] = make_float4(__shfl_xor_sync(kFullMask, j.o[k].x, x), __shfl_xor_sync(kFullMask, j.o[k].y, x),
+                               __shfl_xor_sync(kFullMask, j.o[k].z, x), __shfl_xor_sync(kFullMask, j.o[k].w, x));
+        j.add(make_float2(__shfl_xor_sync(kFullMask, j.M, x), __shfl_xor_sync(kFullMask, j.L, x)), o);
+    }
+    if (parts == 4) return;
+    const int team = threadIdx.x / kTeam, w = threadIdx.x % kTeam / 32, lane = threadIdx.x & 31;
+    if (w > 0 && lane < 8) {
+        sums.ml[team][w - 1][lane] = make_float2(j.M, j.L);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) sums.o[team][w - 1][lane][k] = j.o[k];
+    }
+    team_sync();
+    if (w == 0 && lane < 8) {
+#pragma unroll 1
+        for (int i = 0; i < 3; ++i) j.add(sums.ml[team][i][lane], sums.o[team][i][lane]);
+    }
+    team_sync();  // the sums may be overwritten
+}
+
 // Adds row `srow` of the pieces c0 + part, c0 + part + parts, ... of a cut unit's c0 .. c1, two
 // pieces' reads in flight at a time.  (Short code: it runs once, and every 8 instructions are a
 // fetch.)
@@ -104,15 +144,16 @@ __device__ __forceinline__ void add_span(const SpanParams &p, int s, const Span 
     }
 }
 
-// Shared and own rows, eight lanes per (token, query head), or a warp, whose four groups of eight
-// share a unit's pieces (parts = 4).  p0 is the launch over the shared spans, p1 the one over the own ones.  What bounds it is the chain of reads -- group, lengths,
+// Shared and own rows, 8 * parts threads per (token, query head).  p0 is the launch over the shared
+// spans, p1 the one over the own ones.  What bounds it is the chain of reads -- group, lengths,
 // pieces of the unit, the pieces -- so nothing is looked up by one thread for others.
 template <int D>
 __global__ void __launch_bounds__(256, 3) span_merge_shared_kernel(const __grid_constant__ SpanParams p0, const __grid_constant__ SpanParams p1, int parts) {
+    __shared__ TeamSums<D> sums;
     grid_dependency_wait();
     const int sub = threadIdx.x & 7, part = (threadIdx.x >> 3) & (parts - 1);
     const long long row = (static_cast<long long>(blockIdx.x) * 32 + (threadIdx.x >> 3)) / parts;
-    if (row >= static_cast<long long>(p0.N) * p0.H_q) return;  // whole warps where parts = 4
+    if (row >= static_cast<long long>(p0.N) * p0.H_q) return;  // all threads of a row
     const int tok = static_cast<int>(row / p0.H_q), head = static_cast<int>(row - static_cast<long long>(tok) * p0.H_q);
     const int kvh = head / p0.r, h = head - kvh * p0.r;
     const int b = tok / p0.Q;
@@ -132,37 +173,45 @@ __global__ void __launch_bounds__(256, 3) span_merge_shared_kernel(const __grid_
     Join<D> j;
     if (valid && sg.rows > 0) add_span<D>(p0, g, sg, tok, kvh, h, row, false, sub, part, parts, j);
     if (valid && so.rows > 0) add_span<D>(p1, p1.P + b, so, tok, kvh, h, row, true, sub, part, parts, j);
-    if (parts == 4) {
-#pragma unroll
-        for (int x = 8; x <= 16; x <<= 1) {
-            float4 o[D / 32];
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-                o[k] = make_float4(__shfl_xor_sync(kFullMask, j.o[k].x, x), __shfl_xor_sync(kFullMask, j.o[k].y, x),
-                                   __shfl_xor_sync(kFullMask, j.o[k].z, x), __shfl_xor_sync(kFullMask, j.o[k].w, x));
-            j.add(make_float2(__shfl_xor_sync(kFullMask, j.M, x), __shfl_xor_sync(kFullMask, j.L, x)), o);
-        }
-    }
+    join_parts(j, parts, sums);
     if (part == 0) j.store(p0.out + row * D, sub);
 }
 
-// Cross attention: `slices` warps join the rows of the cut unit that starts in a worker, four at a
-// time, and the tokens whose encoder sequence has no states get zeros.
-template <int D>
+// Cross attention.  `slices` warps (a multiple of a team's four) belong to each worker and join the
+// rows of the cut unit that starts in it, four rows at a time.  SPREAD: a cut unit's rows are divided
+// over the warps of all the workers that have a piece of it, so the more pieces there are to join, the
+// more warps join them.  Tokens whose encoder sequence has no states get zeros.
+template <int D, bool SPREAD>
 __global__ void __launch_bounds__(256, 3) span_merge_cross_kernel(const __grid_constant__ SpanParams p, int slices) {
+    __shared__ TeamSums<D> sums;  // SPREAD
     grid_dependency_wait();
     const int sub = threadIdx.x & 7, warp = blockIdx.x * 8 + (threadIdx.x >> 5);
     const int worker = warp / slices, slice = warp - worker * slices;
     if (worker < p.G) {
-        const SpanRecord u = p.rec[worker];
-        if (u.valid) {
-            const int heads = min(p.rb, p.r - u.hb * p.rb);
-            for (int i = 4 * slice + (threadIdx.x >> 3 & 3); i < u.ntok * heads; i += 4 * slices) {
-                const int tl = i / heads, hp = i - tl * heads;
-                Join<D> j;
-                add_pieces<D>(p, worker, u.k0, u.c1, slot_row(p, tl, hp), sub, 0, 1, j);
-                j.store(p.out + (static_cast<long long>(u.tok0 + tl) * p.H_q + u.kvh * p.r + u.hb * p.rb + hp) * D, sub);
+        SpanRecord u = p.rec[worker];
+        const int cont = SPREAD ? u.cont : -1;
+        int c0 = worker;
+#pragma unroll 1
+        while (true) {  // the unit that starts here and the one that this worker's first piece goes on with
+            if (u.valid) {
+                const int heads = min(p.rb, p.r - u.hb * p.rb), rows = u.ntok * heads, n = SPREAD ? u.c1 - c0 + 1 : 1;
+                const int parts = !SPREAD ? 1 : rows * 4 <= n * slices ? 16 : rows <= n * slices ? 4 : 1;
+                // among the unit's groups of eight threads
+                const int group = ((worker - c0) * slices + slice) * 4 + (threadIdx.x >> 3 & 3);
+                const int part = group & (parts - 1);
+#pragma unroll 1
+                for (int i = group / parts; i < rows; i += n * slices * 4 / parts) {
+                    const int tl = i / heads, hp = i - tl * heads;
+                    Join<D> j;
+                    add_pieces<D>(p, c0, u.k0, u.c1, slot_row(p, tl, hp), sub, part, parts, j);
+                    if constexpr (SPREAD) join_parts(j, parts, sums);
+                    if (part == 0)
+                        j.store(p.out + (static_cast<long long>(u.tok0 + tl) * p.H_q + u.kvh * p.r + u.hb * p.rb + hp) * D, sub);
+                }
             }
+            if (cont < 0 || c0 == cont) break;
+            c0 = cont;
+            u = p.rec[c0];
         }
     }
     for (int e = blockIdx.x; e < p.P; e += gridDim.x) {
@@ -193,16 +242,20 @@ int launch_span_merge(const SpanParams &shared, const SpanParams &own, cudaStrea
     const SpanParams &p = shared;
     if (own.B > 0) {
         // With few rows the shared spans are cut into many pieces (19 for 16 sequences over 8
-        // key/value heads: 14 us by eight lanes a row, 9 by a warp) and there are SMs enough for a
-        // warp a row; 8192 rows of few pieces take 11 us by eight lanes and 19 by a warp.
+        // key/value heads: 14 us by eight lanes a row, 9 by a warp; 148 for 2 sequences under one
+        // prompt of 4096 rows: the call takes 32 us by a warp, 20 by a team) and there are SMs enough;
+        // 8192 rows of few pieces take 11 us by eight lanes and 19 by a warp.
         const long long rows = static_cast<long long>(p.N) * p.H_q;
-        const int parts = rows <= 2048 ? 4 : 1;
+        const int parts = rows <= 512 ? 16 : rows <= 2048 ? 4 : 1;
         const dim3 grid(static_cast<unsigned>((rows * parts + 31) / 32));
         return p.d == 128 ? launch(span_merge_shared_kernel<128>, grid, stream, p, own, parts) : launch(span_merge_shared_kernel<64>, grid, stream, p, own, parts);
     }
-    const int slices = (p.unit_rows + 3) / 4;  // warps that take a full unit's rows at once
+    // Warps that take a full unit's rows at once: a multiple of four, as unit_rows is 16 times something.
+    const int slices = p.unit_rows / 4;
     const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.G) * slices + 7) / 8));
-    return p.d == 128 ? launch(span_merge_cross_kernel<128>, grid, stream, p, slices) : launch(span_merge_cross_kernel<64>, grid, stream, p, slices);
+    if (p.spread)
+        return p.d == 128 ? launch(span_merge_cross_kernel<128, true>, grid, stream, p, slices) : launch(span_merge_cross_kernel<64, true>, grid, stream, p, slices);
+    return p.d == 128 ? launch(span_merge_cross_kernel<128, false>, grid, stream, p, slices) : launch(span_merge_cross_kernel<64, false>, grid, stream, p, slices);
 }
 
 }  // namespace gqa

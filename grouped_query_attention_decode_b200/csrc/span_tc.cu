@@ -37,6 +37,12 @@
 //   warps 4..11 softmax, sums and epilogue: stream (warp - 4) / 4, a row a thread
 // Every wait is bounded; on a timeout the CTA drains its copies and UMMAs, frees its tensor
 // memory, sets GQA_STATUS_WAIT_TIMEOUT and returns.
+//
+// Measured (one B200): 4 x 1024 tokens over 4096 states, 64/8 heads, d = 128 take 666-685 us in a
+// graph, 803-825 TFLOP/s of attention and 1.5 times that of products.  A step of 128 x 128 scores
+// is ~2400 cycles where its products alone are 2060 (scores 780, bound by reading both operands from
+// shared memory; P.V 1280) and a softmax warp's chain is 2465; the tensor pipe is active 52 % of
+// the time, DRAM 10 %.
 #include <cstdint>
 
 #include "device.cuh"

@@ -56,10 +56,13 @@ struct SpanParams {
     int behind_shared;     // few rows: launched behind the launch over the shared spans (span_few.cu)
     int u1;                // number of the own spans' first token block, after the shared spans'
     int unit_rows;         // query rows of a slot
+    int spread;            // cross attention: units are cut into many pieces (span_merge.cu)
 };
 
 struct SpanRecord {
-    int valid, tok0, ntok, kvh, hb, k0, c1, pad;
+    int valid, tok0, ntok, kvh, hb, k0, c1;
+    int cont;  // with `spread`: the worker that starts the cut unit which this one's first piece goes on
+               // with, or -1
 };
 
 // The group that member i belongs to, -1 for none: the last g with gstart[g] <= i.
@@ -331,17 +334,30 @@ __device__ __forceinline__ int seen_rows(const SpanParams &p, const SpanSegment 
 
 // One thread of worker `cta` (a CTA, or a warp of span_few.cu), before its segments.
 __device__ __forceinline__ void open_notes(const SpanParams &p, int cta) {
-    if (p.B == 0) p.rec[cta].valid = 0;
+    if (p.B == 0) {
+        p.rec[cta].valid = 0;
+        p.rec[cta].cont = -1;  // not read without `spread`
+    }
 }
 
 // The same thread, once per segment: what the merge needs to find the unit's pieces.
 __device__ inline void note_unit(const SpanParams &p, const SpanSegment &g, const SpanRange &cr, int c0) {
-    if (g.j0 != 0) return;
+    if (g.j0 != 0) {
+        if (p.spread) p.rec[c0].cont = static_cast<int>(cta_of_tile(g.uoff, cr.total, cr.parts));
+        return;
+    }
     const int c1 = g.whole() ? c0 : static_cast<int>(cta_of_tile(g.uoff + g.nt - 1, cr.total, cr.parts));
     if (p.B > 0) {  // there are own rows to join with, here or in another launch
         p.uinfo[g.unit] = make_int4(c0, g.first ? 0 : 1, c1, 0);
     } else if (!g.whole()) {
-        p.rec[c0] = SpanRecord{1, g.tok0, g.ntok, g.kvh, g.hb, g.first ? 0 : 1, c1, 0};
+        SpanRecord &u = p.rec[c0];
+        u.tok0 = g.tok0;
+        u.ntok = g.ntok;
+        u.kvh = g.kvh;
+        u.hb = g.hb;
+        u.k0 = g.first ? 0 : 1;
+        u.c1 = c1;
+        u.valid = 1;
     }
 }
 
@@ -360,9 +376,12 @@ int launch_span_f32(const SpanParams &p, const float *q, const float *ks, const 
 // Joins the pieces of one launch over the shared spans and one over the own ones (the same launch,
 // or none: own.B = 0).
 int launch_span_merge(const SpanParams &shared, const SpanParams &own, cudaStream_t stream);
-// The kernel for few query rows per span; p.G is the number of warps (span_few_warps a CTA), k and v
+// The kernel for few query rows per span; p.G is the number of warps (span_few_warps a CTA), K and V
 // are copied in boxes of 8 rows.
-int launch_span_few(const SpanParams &p, const CUtensorMap &k, const CUtensorMap &v, const void *q, cudaStream_t stream);
+struct SpanFewMaps {
+    CUtensorMap kv[4];  // K and V of the shared rows, K and V of the own ones
+};
+int launch_span_few(const SpanParams &p, const SpanFewMaps &maps, const void *q, cudaStream_t stream);
 int span_few_warps(int d);
 
 }  // namespace gqa

@@ -324,8 +324,9 @@ int gqa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
  * drafts NaN, those before it included.  bfloat16 (tensor cores) and float32 (CUDA cores).  P >= 1;
  * d, heads and alignment as for gqa_decode.  The workspace needs
  * gqa_decode_shared_workspace_size() bytes and no zero-fill; two calls that may run at the same
- * time must not share one.  Launches two kernels on `stream`, three when a sequence has at most 32
- * query rows (16 for float32) per key/value head: the shared rows, the own rows, and what joins them.
+ * time must not share one.  Launches two or three kernels on `stream`: the shared rows and the own
+ * rows, together or (few query rows of own rows, many of shared ones) one after the other, and what
+ * joins them.
  */
 size_t gqa_decode_shared_workspace_size(int B, int Q, int P, int H_q, int H_kv, int d,
                                         gqa_dtype_t dtype);
