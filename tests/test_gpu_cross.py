@@ -149,6 +149,21 @@ def test_few_tokens_out_of_range(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [[1], [3, 0, 1], [40]], ids=str)
+@pytest.mark.parametrize("heads", [(8, 1, 128), (12, 4, 64)], ids=lambda h: "%d_%d_%d" % h)
+def test_many_pieces(heads, tokens, dtype):
+    """Spans cut into far more pieces than there are query rows, one of them among empty ones."""
+    x = make(tokens, [20001, 5, 0][:len(tokens)], heads, dtype, behind=1)
+    ws = torch.full((gqa.cross_workspace_size(len(tokens), x["q"].shape[0], *heads, dtype),), 255, dtype=torch.uint8, device="cuda")
+    out, status = run(x, 0.1, workspace=ws)
+    assert status == 0
+    check(x, out, 0.1)
+    again, _ = run(x, 0.1, workspace=ws)
+    n = x["starts"][-1]
+    assert torch.equal(out[:n], again[:n])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_few_tokens_repeat(dtype):
     # the workspace's counters are set anew by each call
     x = make([1] * 5, [700, 3, 2000, 129, 0], (16, 4, 128), dtype)
