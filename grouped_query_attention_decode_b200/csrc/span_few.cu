@@ -9,9 +9,9 @@
 //
 //   S[16 x 16] = Q[16 x d] . K_tile^T,  O[16 x d] += P[16 x 16] . V_tile    (mma m16n8k16)
 //
-// The products are a few percent of what the memory takes, so the warp-level mma, whose operands
-// and results are in the registers of the one warp that needs them, costs nothing against tcgen05
-// and saves its round trips through tensor memory.  P enters as two bf16 parts (the outputs are
+// The products keep the tensor pipe active a quarter of the time, so the warp-level mma, whose
+// operands and results are in the registers of the one warp that needs them, is fast enough and
+// saves tcgen05's round trips through tensor memory.  P enters as two bf16 parts (the outputs are
 // float32), each tile's P.V starts from zero and is added in fp32, rounded to nearest.
 //
 // Measured (one B200): 32 sequences of 1024 states, 64/64 heads, d = 64, one token each: 537 MB in
