@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(256, 3) span_merge_shared_kernel(const __grid_
     Span sg = {0, 0, 0, 0, 0}, so = {b * p0.Q, p0.Q, 0, 0, 0};
     bool valid = true;
     if (g >= 0) {
-        sg = span_at(p0, g, false);
+        sg = span_at(p0, g, false, false);  // a row that is valid has a holder in its group: its sequence
         valid = shared_rows_of(p0, g) >= 0;
         if (p1.own_after) so.row0 = max(sg.rows, 0);
         if (tok < sg.tok0 || tok >= sg.tok0 + sg.ntok) sg.rows = 0;  // a group whose start is out of range

@@ -98,13 +98,28 @@ __device__ __forceinline__ bool own_rows_of(const SpanParams &p, int b, int &row
     return true;
 }
 
+// Paged caches: the first sequence of [a, e) whose length is one that own_rows_of takes behind `shared`
+// rows, so its table holds them; -1 for none (all have ended).  One length at a time: the kernels inline
+// this in many places, and longer code, fetched once a call, costs more than it saves (four at a time:
+// 131 us for 127 at 128 conversations under 12032 rows).
+__device__ __forceinline__ int holder_of(const int32_t *lens, int a, int e, int least, int most) {
+#pragma unroll 1
+    for (int i = a; i < e; ++i) {
+        const int n = __ldg(lens + i);
+        if (n >= least && n <= most) return i;
+    }
+    return -1;
+}
+
 struct Span {
     int tok0, ntok;  // its tokens
     int row0, rows;  // its cached rows within the source
     int src;         // contiguous: prefix / encoder sequence / sequence; paged: block-table row
 };
 
-__device__ inline Span span_at(const SpanParams &p, int s, bool flag) {
+// `table`: false where the span's block-table row is not asked for; then the shared rows of a group that
+// has ended are counted too.
+__device__ inline Span span_at(const SpanParams &p, int s, bool flag, bool table = true) {
     Span sp = {0, 0, 0, 0, 0};
     int bad = 0;
     if (s < p.P) {
@@ -117,7 +132,11 @@ __device__ inline Span span_at(const SpanParams &p, int s, bool flag) {
             sp.tok0 = a * p.Q;
             sp.ntok = (e - a) * p.Q;
             sp.rows = max(n, 0);
-            sp.src = p.block_table != nullptr ? a : s;
+            sp.src = s;
+            if (p.block_table != nullptr && table && sp.rows > 0) {
+                sp.src = holder_of(p.lens, a, e, sp.rows + (p.Q > 1 ? p.Q : 0), p.own_max);
+                if (sp.src < 0) sp.src = sp.rows = 0;
+            }
         }
     } else if (s < p.P + p.B) {
         const int b = s - p.P;

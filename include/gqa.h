@@ -312,9 +312,10 @@ int gqa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
  * gqa_decode_shared_paged: the result of gqa_decode_paged (for Q > 1: of gqa_decode_multi) over
  *   the same pools, block_table [B][max_pages] and seq_lens, for tables in which the sequences of
  *   group g hold their first shared_rows[g] rows in the same pages (as gqa_pages_fork leaves
- *   them).  Those rows are read through the table of the group's first sequence, which has to hold
- *   them.  shared_rows[g] must be a multiple of page_size and at most seq_lens[b] (- Q for Q > 1) of
- *   every sequence of the group; an empty sequence (seq_lens[b] = 0, Q = 1) gets zeros.
+ *   them).  shared_rows[g] must be a multiple of page_size and at most seq_lens[b] (- Q for Q > 1) of
+ *   every sequence of the group; an empty sequence (seq_lens[b] = 0, Q = 1) gets zeros.  The shared
+ *   rows are read through the table of the group's first sequence whose length is so, so members
+ *   that have ended may stay, the first among them; a group of ended sequences alone reads nothing.
  *   page_size must be a multiple of 8 and divide 128 or be a multiple of 128 (any multiple of 8
  *   for float32).
  * A length out of range -- negative, past its capacity, own rows < Q (Q > 1), shared rows that do
