@@ -626,7 +626,8 @@ def pages_free(seqs, block_table, seq_lens, ref_counts, status=None, stream=None
 def pages_reserve(block_table, seq_lens, ref_counts, rows: int, page_size: int, copies=None,
                   workspace=None, status=None, stream=None) -> torch.Tensor:
     """gqa_pages_reserve: every sequence gets pages of its own for its next ``rows`` rows.  Returns
-    copies [B, 2] (old page, new page; -1: none), for pages_copy."""
+    copies [B, 2] (old page, new page; -1: none): run pages_copy on them in every layer before the
+    next change, when the pool ran out (STATUS_POOL_FULL) too."""
     lib = _lib or load_library()
     B, max_pages = block_table.shape
     n_pages = ref_counts.shape[0]

@@ -378,7 +378,7 @@ int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const 
  *                               aligned for gqa_pages_reserve and gqa_pages_compact
  * An empty pool is counts of zero and tables of -1.  One table serves every layer of a model: the
  * calls below that move pages write the moves down as pairs (from, to), and gqa_pages_copy
- * carries them out in one layer's pools.  Every result is determined by the inputs (free pages
+ * carries them out in one layer's pools, before the next of these calls.  Every result is determined by the inputs (free pages
  * are taken lowest number first).  A table entry outside [-1, n_pages) counts as -1 and sets
  * GQA_STATUS_PAGE_RANGE; counts that do not belong to the tables set GQA_STATUS_PAGE_REFS where
  * that is noticed.
@@ -395,11 +395,13 @@ int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const 
  *   seq_lens[b] + rows): a new page where it has none, and in the place of a page that others hold
  *   too (copy on write) -- except that when every holder is about to write it, the last of them
  *   keeps it.  copies [B][2] gets (old, new) where rows of the old page have to be copied, else
- *   (-1, -1): run gqa_pages_copy on it before appending.  The lengths do not change.  A sequence
- *   whose rows do not fit max_pages * page_size gets nothing (GQA_STATUS_APPEND_OVERFLOW).  When
- *   free pages run out, the first sequence that they do not suffice for and those behind it that
- *   need any get none (GQA_STATUS_POOL_FULL), and rows about to be written may still lie in shared
- *   pages: append to no sequence then, but free pages and call again.
+ *   (-1, -1): run gqa_pages_copy on it, in every layer, before anything else changes the tables,
+ *   the counts or the pools, and whatever the status says.  A pair stands in the copies of one call
+ *   only.  The lengths do not change.  A sequence whose rows do not fit max_pages * page_size gets
+ *   nothing (GQA_STATUS_APPEND_OVERFLOW).  When free pages run out, the first sequence that they do
+ *   not suffice for and those behind it that need any get none (GQA_STATUS_POOL_FULL), and rows
+ *   about to be written may still lie in shared pages: append to no sequence then, but carry out
+ *   the copies (the sequences before have their new pages already), free pages and call again.
  * gqa_pages_compact: moves the pages in use to the front of the pool.  With n of them, the pages
  *   numbered n and up, in ascending order, take the places of the free ones below n; tables and
  *   counts follow, copies [max(1, n_pages / 2)][2] gets the moves, (-1, -1) behind the last, and
