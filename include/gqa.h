@@ -402,6 +402,10 @@ int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const 
  *   not suffice for and those behind it that need any get none (GQA_STATUS_POOL_FULL), and rows
  *   about to be written may still lie in shared pages: append to no sequence then, but carry out
  *   the copies (the sequences before have their new pages already), free pages and call again.
+ *   An empty sequence is one that begins: it gets its first page, and an append makes it one row
+ *   long, which is shorter than what its group shares (GQA_STATUS_SEQLEN_RANGE in the decode).  So
+ *   empty a sequence that has ended -- parent -1 in a fork, or gqa_pages_free -- again behind every
+ *   append that it takes part in, before the decode, and keep a free page for it.
  * gqa_pages_compact: moves the pages in use to the front of the pool.  With n of them, the pages
  *   numbered n and up, in ascending order, take the places of the free ones below n; tables and
  *   counts follow, copies [max(1, n_pages / 2)][2] gets the moves, (-1, -1) behind the last, and

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import grouped_query_attention_decode_b200 as gqa
+from span_ref import attend64, normal, tolerance
 from test_gpu_shared import expect, make, paged, tol
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +97,50 @@ def test_drafts_of_the_members_that_are_left(dtype):
     out, status = decode(x, [0], lambda table, lens, b: lens.__setitem__(b, 64 + 2))
     assert status == gqa.STATUS_SEQLEN_RANGE
     check(x, out, [0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_beams_that_end(dtype):
+    """Beams of two prompts that fork and end, the first of a prompt among them: fork, reserve, copy,
+    append, free the ended ones, decode; each live beam against float64 over its own rows."""
+    H_q, H_kv, d, ps, n_pages, max_pages, B, scale = 16, 2, 64, 8, 120, 12, 10, 0.2
+    g = torch.Generator().manual_seed(4)
+    k_pool = torch.full((n_pages, ps, H_kv, d), float("nan"), dtype=dtype, device="cuda")
+    v_pool = k_pool.clone()
+    state = [(torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda"), i32([0] * B)) for _ in range(2)]
+    refs, status = i32([0] * n_pages), i32([0])
+    rows = [([], []) for _ in range(B)]
+    starts, shared = i32([0, 5, 10]), i32([32, 40])
+    # beams 0 and 5 are the prompts at first; from step 45 on every second step forks and ends beams
+    ended, forks = [], {45: [0] * 5 + [5] * 5, 47: [-1, 2, 1, 2, 1, 6, 6, -1, 9, 5], 49: [-1, -1, 3, 4, 4, -1, 5, -1, 8, 6],
+                        51: [-1] * 5 + [6, -1, -1, 8, 9]}
+    for t in range(55):
+        if t in forks:
+            (table, lens), (table2, lens2) = state
+            gqa.pages_fork(i32(forks[t]), table, lens, table2, lens2, refs, status=status)
+            state.reverse()
+            ended = [b for b, p in enumerate(forks[t]) if p < 0]
+            rows = [([], []) if p < 0 else (list(rows[p][0]), list(rows[p][1])) for p in forks[t]]
+        table, lens = state[0]
+        gqa.pages_copy(k_pool, v_pool, gqa.pages_reserve(table, lens, refs, 1, ps, status=status))
+        kn, vn = normal((B, H_kv, d), g, dtype), normal((B, H_kv, d), g, dtype)
+        gqa.kv_append_paged(kn.cuda(), vn.cuda(), k_pool, v_pool, table, lens, status=status)
+        for b in range(B):
+            rows[b][0].append(kn[b])
+            rows[b][1].append(vn[b])
+        if ended:
+            gqa.pages_free(i32(ended), table, lens, refs, status=status)
+        if t >= 45:
+            q = normal((B, H_q, d), g, dtype)
+            out = gqa.decode_shared_paged(q.cuda(), k_pool, v_pool, table, lens, starts, shared, scale, status=status)
+            assert int(status) == 0
+            for b in range(B):
+                if b in ended:
+                    assert not out[b].any() and not int(lens[b])
+                    continue
+                k, v = torch.stack(rows[b][0]).cuda(), torch.stack(rows[b][1]).cuda()
+                assert int(lens[b]) == len(k)
+                err = float((out[b].double() - attend64(q[b].cuda(), k, v, scale)).abs().max())
+                assert err <= tolerance(q, [k], [v], scale, len(k)), (t, b, err)
+    want = torch.bincount(state[0][0][state[0][0] >= 0].long(), minlength=n_pages)
+    assert torch.equal(want.int(), refs)
