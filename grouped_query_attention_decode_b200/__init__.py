@@ -428,9 +428,14 @@ def decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
 
 # ------------------------------------------------------------------ rows that sequences share
 # Small calls are bound by the host, so what follows makes few Python calls per argument.
-def _tensors(first: torch.Tensor, *tensors) -> int:
-    """The device number of ``first``; every tensor (None: absent) has to be dense and on it."""
+def _tensors(status, first: torch.Tensor, *tensors) -> int:
+    """The device number of ``first``; every tensor (None: absent) has to be dense and on it, and
+    ``status`` hold the word that a kernel may write."""
     dev = first.get_device()
+    if status is not None:
+        if status.dtype is not torch.int32 or status.numel() < 1:
+            raise ValueError(f"status must be torch.int32 of one element or more, not {status.dtype} {list(status.shape)}")
+        tensors += (status,)
     if dev < 0:
         raise ValueError("libgqa needs CUDA tensors")
     if not first.is_contiguous():
@@ -517,7 +522,7 @@ def decode_shared(q, k_prefix, v_prefix, prefix_lens, group_start, k_cache, v_ca
     _want(prefix_lens, (P,), torch.int32, "prefix_lens")
     _want(group_start, (P + 1,), torch.int32, "group_start")
     _want(seq_lens, (B,), torch.int32, "seq_lens")
-    dev = _tensors(q, k_prefix, v_prefix, prefix_lens, group_start, k_cache, v_cache, seq_lens, out, workspace, status)
+    dev = _tensors(status, q, k_prefix, v_prefix, prefix_lens, group_start, k_cache, v_cache, seq_lens, out, workspace)
     if out is None:
         out = _made(torch.empty_like(q, dtype=torch.float32), stream)
     else:
@@ -547,7 +552,7 @@ def decode_shared_paged(q, k_pool, v_pool, block_table, seq_lens, group_start, s
     _want(seq_lens, (B,), torch.int32, "seq_lens")
     _want(group_start, (P + 1,), torch.int32, "group_start")
     _want(shared_rows, (P,), torch.int32, "shared_rows")
-    dev = _tensors(q, k_pool, v_pool, block_table, seq_lens, group_start, shared_rows, out, workspace, status)
+    dev = _tensors(status, q, k_pool, v_pool, block_table, seq_lens, group_start, shared_rows, out, workspace)
     if out is None:
         out = _made(torch.empty_like(q, dtype=torch.float32), stream)
     else:
@@ -579,7 +584,7 @@ def cross_attend(q, k_enc, v_enc, enc_lens, q_start, scale: float, out=None, wor
     _want(v_enc, (E, S_max, H_kv, d), dtype, "v_enc")
     _want(enc_lens, (E,), torch.int32, "enc_lens")
     _want(q_start, (E + 1,), torch.int32, "q_start")
-    dev = _tensors(q, k_enc, v_enc, enc_lens, q_start, out, workspace, status)
+    dev = _tensors(status, q, k_enc, v_enc, enc_lens, q_start, out, workspace)
     if out is None:
         out = _made(torch.empty_like(q, dtype=torch.float32), stream)
     else:
@@ -604,7 +609,7 @@ def pages_fork(parents, table_in, lens_in, table_out, lens_out, ref_counts, stat
     _want(lens_out, (B_out,), torch.int32, "lens_out")
     _want(parents, (B_out,), torch.int32, "parents")
     _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
-    dev = _tensors(table_in, parents, lens_in, table_out, lens_out, ref_counts, status)
+    dev = _tensors(status, table_in, parents, lens_in, table_out, lens_out, ref_counts)
     _run(dev, lib.gqa_pages_fork, parents.data_ptr(), table_in.data_ptr(), lens_in.data_ptr(), B_in, table_out.data_ptr(),
          lens_out.data_ptr(), B_out, max_pages, ref_counts.data_ptr(), n_pages, _addr(status), _raw_stream(stream, dev))
 
@@ -618,7 +623,7 @@ def pages_free(seqs, block_table, seq_lens, ref_counts, status=None, stream=None
     _want(block_table, (B, max_pages), torch.int32, "block_table")
     _want(seq_lens, (B,), torch.int32, "seq_lens")
     _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
-    dev = _tensors(block_table, seqs, seq_lens, ref_counts, status)
+    dev = _tensors(status, block_table, seqs, seq_lens, ref_counts)
     _run(dev, lib.gqa_pages_free, seqs.data_ptr(), n, block_table.data_ptr(), seq_lens.data_ptr(), B, max_pages,
          ref_counts.data_ptr(), n_pages, _addr(status), _raw_stream(stream, dev))
 
@@ -634,7 +639,7 @@ def pages_reserve(block_table, seq_lens, ref_counts, rows: int, page_size: int, 
     _want(block_table, (B, max_pages), torch.int32, "block_table")
     _want(seq_lens, (B,), torch.int32, "seq_lens")
     _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
-    dev = _tensors(block_table, seq_lens, ref_counts, copies, workspace, status)
+    dev = _tensors(status, block_table, seq_lens, ref_counts, copies, workspace)
     if copies is None:
         copies = _made(torch.empty((B, 2), dtype=torch.int32, device=block_table.device), stream)
     else:
@@ -655,7 +660,7 @@ def pages_compact(block_table, ref_counts, copies=None, n_live=None, workspace=N
     n_pages = ref_counts.shape[0]
     _want(block_table, (B, max_pages), torch.int32, "block_table")
     _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
-    dev = _tensors(block_table, ref_counts, copies, n_live, workspace, status)
+    dev = _tensors(status, block_table, ref_counts, copies, n_live, workspace)
     most = max(1, n_pages // 2)
     if copies is None:
         copies = _made(torch.empty((most, 2), dtype=torch.int32, device=block_table.device), stream)
@@ -683,6 +688,6 @@ def pages_copy(k_pool, v_pool, copies, status=None, stream=None) -> None:
     n = copies.shape[0]
     _want(v_pool, k_pool.shape, k_pool.dtype, "v_pool")
     _want(copies, (n, 2), torch.int32, "copies")
-    dev = _tensors(k_pool, v_pool, copies, status)
+    dev = _tensors(status, k_pool, v_pool, copies)
     _run(dev, lib.gqa_pages_copy, k_pool.data_ptr(), v_pool.data_ptr(), copies.data_ptr(), n, page_size, n_pages, H_kv, d, code,
          _addr(status), _raw_stream(stream, dev))
