@@ -5,8 +5,9 @@
 // RT/16 x 4 scores and RT/16 x d/16 sums, and a query row's 16 threads are half a warp, which takes
 // its maximum and sum by shuffles.  With 64 rows the two products read 8 (16) values from shared
 // memory per 16 (32) fused multiply-adds of a thread and run at 35 TFLOP/s (4 encoder sequences of
-// 2048 rows under 256 tokens, 32/8 heads, d = 128: 980 us).  With 16 rows they are bound by those
-// reads and by issue, so warps whose rows are padding leave them out: 16 sequences of 4000 rows
+// 2048 rows under 256 tokens, 32/8 heads, d = 128: 980 us), half of what the CUDA cores have: one CTA
+// fits an SM, two warps a scheduler, and so few hide little of each other's reads.  With 16 rows
+// they are bound by those reads and by issue, so warps whose rows are padding leave them out: 16 sequences of 4000 rows
 // under 4 rows a head take 130 us (82 at the speed of memory), 302 with every warp at work.
 #include <cstdint>
 

@@ -38,11 +38,15 @@
 // Every wait is bounded; on a timeout the CTA drains its copies and UMMAs, frees its tensor
 // memory, sets GQA_STATUS_WAIT_TIMEOUT and returns.
 //
-// Measured (one B200): 4 x 1024 tokens over 4096 states, 64/8 heads, d = 128 take 666-685 us in a
-// graph, 803-825 TFLOP/s of attention and 1.5 times that of products.  A step of 128 x 128 scores
+// Measured (one B200): 4 x 1024 tokens over 4096 states, 64/8 heads, d = 128 take 666-690 us in a
+// graph, 797-825 TFLOP/s of attention and 1.5 times that of products.  A step of 128 x 128 scores
 // is ~2400 cycles where its products alone are 2060 (scores 780, bound by reading both operands from
-// shared memory; P.V 1280) and a softmax warp's chain is 2465; the tensor pipe is active 52 % of
-// the time, DRAM 10 %.
+// shared memory; P.V 1280) and a softmax warp's chain is 2465.  There a CTA has 444 steps and they
+// account for the time; with a few tens of steps they do not: 8 ragged targets of up to 509 tokens
+// over up to 2047 states (32/8 heads) have at most 38 a CTA, 50 us, and take 84.  About 8 us are the
+// start; the rest is not attributed (a CTA has two to four pieces there, and a stream's warps finish
+// one before they look at the next one's scores).  Of 4 x 128 tokens over 4096 states, 56 steps, the
+// tensor pipe is active 52 % of the time, DRAM 10 %.
 #include <cstdint>
 
 #include "device.cuh"

@@ -301,8 +301,10 @@ int gqa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
  *
  * Group g (0 <= g < P) is the sequences [group_start[g], group_start[g + 1]); group_start [P + 1]
  * int32 (device) must not decrease and must lie in [0, B] (GQA_STATUS_GROUP_RANGE otherwise).
- * Sequences outside every group share nothing.  q [B][Q][H_q][d] holds Q query tokens per
- * sequence, 1 <= Q <= 32, which are the last Q of its own rows, as in gqa_decode_multi.  out
+ * Sequences outside every group share nothing.  There is one level of sharing: where prompts with
+ * samples of their own stand under one system prompt, a group is either the samples of a prompt,
+ * whose rows then include the system prompt's, or all of them, who share the system prompt alone.
+ * q [B][Q][H_q][d] holds Q query tokens per sequence, 1 <= Q <= 32, which are the last Q of its own rows, as in gqa_decode_multi.  out
  * [B][Q][H_q][d] float32.
  *
  * gqa_decode_shared: contiguous caches.  The rows that group g shares are k_prefix, v_prefix
@@ -322,7 +324,13 @@ int gqa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
  * not fit the rules above -- gives out[b] = 0 for the sequences concerned and sets
  * GQA_STATUS_SEQLEN_RANGE.  Cached rows that no token of a sequence sees are never read into a
  * result; a drafted token's row that is not finite can make the outputs of the sequence's other
- * drafts NaN, those before it included.  bfloat16 (tensor cores) and float32 (CUDA cores).  P >= 1;
+ * drafts NaN, those before it included.  bfloat16 (tensor cores) and float32 (CUDA cores).  In
+ * bfloat16 a softmax weight enters the product with V as two bfloat16 parts (~16 bits), so an
+ * infinite element of a V row that is seen can come out as NaN instead of infinity.
+ * Which kernel reads the shared rows follows from sizes that the host has: the mean number of
+ * query rows, B * Q / P * H_q / H_kv, empty groups counted.  Results do not depend on it, time
+ * does, so let P be the number of groups in use: 128 sequences under 2048 rows take 52 us, and
+ * 162 us with 63 empty groups beside theirs.  P >= 1;
  * d, heads and alignment as for gqa_decode.  The workspace needs
  * gqa_decode_shared_workspace_size() bytes and no zero-fill; two calls that may run at the same
  * time must not share one.  Launches two or three kernels on `stream`: the shared rows and the own
@@ -358,7 +366,10 @@ int gqa_decode_shared_paged(const void *q, const void *k_pool, const void *v_poo
  *   q_start  [E + 1] int32, must not decrease and must lie in [0, N] (GQA_STATUS_GROUP_RANGE
  *            otherwise, and that sequence's tokens are not written).  Tokens before q_start[0] and
  *            from q_start[E] on are neither read nor written.
- * Types, d, heads, alignment and errors as gqa_decode; the workspace needs
+ * Types, d, heads, alignment and errors as gqa_decode, infinite values as gqa_decode_shared.  The
+ * kernel follows from the mean number of tokens, N / E: a few much longer targets among many of
+ * one token are better served by a call of their own (63 tokens and a target of 190 over 2000
+ * states each, 64/8 heads, d = 128: 178 us in one call, 133 in two).  The workspace needs
  * gqa_cross_attend_workspace_size() bytes and no zero-fill; two calls that may run at the same
  * time must not share one.  Launches two kernels on `stream`.
  */
