@@ -615,7 +615,7 @@ def pages_fork(parents, table_in, lens_in, table_out, lens_out, ref_counts, stat
 
 
 def pages_free(seqs, block_table, seq_lens, ref_counts, status=None, stream=None) -> None:
-    """gqa_pages_free: empty the sequences listed in ``seqs`` (int32 [n])."""
+    """gqa_pages_free: empty the sequences listed in ``seqs`` (int32 [n]; none: nothing is done)."""
     lib = _lib or load_library()
     B, max_pages = block_table.shape
     n, n_pages = seqs.shape[0], ref_counts.shape[0]
@@ -624,6 +624,8 @@ def pages_free(seqs, block_table, seq_lens, ref_counts, status=None, stream=None
     _want(seq_lens, (B,), torch.int32, "seq_lens")
     _want(ref_counts, (n_pages,), torch.int32, "ref_counts")
     dev = _tensors(status, block_table, seqs, seq_lens, ref_counts)
+    if n == 0:
+        return
     _run(dev, lib.gqa_pages_free, seqs.data_ptr(), n, block_table.data_ptr(), seq_lens.data_ptr(), B, max_pages,
          ref_counts.data_ptr(), n_pages, _addr(status), _raw_stream(stream, dev))
 
@@ -678,7 +680,7 @@ def pages_compact(block_table, ref_counts, copies=None, n_live=None, workspace=N
 
 def pages_copy(k_pool, v_pool, copies, status=None, stream=None) -> None:
     """gqa_pages_copy: carry out ``copies`` [n, 2] (from, to) in the pools of one layer,
-    [n_pages, page_size, H_kv, d] of bfloat16, float32 or e4m3 codes."""
+    [n_pages, page_size, H_kv, d] of bfloat16, float32 or e4m3 codes; no copies: nothing is done."""
     lib = _lib or load_library()
     if k_pool.dtype in _DTYPES:
         code = _DTYPES[k_pool.dtype]
@@ -689,5 +691,7 @@ def pages_copy(k_pool, v_pool, copies, status=None, stream=None) -> None:
     _want(v_pool, k_pool.shape, k_pool.dtype, "v_pool")
     _want(copies, (n, 2), torch.int32, "copies")
     dev = _tensors(status, k_pool, v_pool, copies)
+    if n == 0:
+        return
     _run(dev, lib.gqa_pages_copy, k_pool.data_ptr(), v_pool.data_ptr(), copies.data_ptr(), n, page_size, n_pages, H_kv, d, code,
          _addr(status), _raw_stream(stream, dev))

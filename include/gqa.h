@@ -400,8 +400,8 @@ int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const 
  *   takes as a parent are freed; afterwards table_out is the state and table_in is not.  Input and
  *   output arrays must not overlap (GQA_ERR_OVERLAP).  A parent outside [-1, B_in) counts as -1
  *   and sets GQA_STATUS_INDEX_RANGE.
- * gqa_pages_free: empties the n sequences listed in seqs (a sequence listed twice is freed once;
- *   a number outside [0, B) is skipped, GQA_STATUS_INDEX_RANGE).
+ * gqa_pages_free: empties the n >= 1 sequences listed in seqs (a sequence listed twice is freed
+ *   once, and an empty one stays so; a number outside [0, B) is skipped, GQA_STATUS_INDEX_RANGE).
  * gqa_pages_reserve: gives every sequence pages of its own for its next `rows` rows, [seq_lens[b],
  *   seq_lens[b] + rows): a new page where it has none, and in the place of a page that others hold
  *   too (copy on write) -- except that when every holder is about to write it, the last of them
@@ -422,7 +422,7 @@ int gqa_cross_attend(const void *q, const void *k_enc, const void *v_enc, const 
  *   counts follow, copies [max(1, n_pages / 2)][2] gets the moves, (-1, -1) behind the last, and
  *   n_live [1] gets n.
  * gqa_pages_copy: copies page from to page to in k_pool and v_pool [n_pages][page_size][H_kv][d]
- *   for each of the n pairs; (-1, -1) is skipped, another pair outside the pool too, with
+ *   for each of the n >= 1 pairs; (-1, -1) is skipped, another pair outside the pool too, with
  *   GQA_STATUS_INDEX_RANGE.  The pages written must be distinct and not among those read.  Any
  *   dtype, GQA_DTYPE_E4M3 included.
  * The workspace of gqa_pages_reserve and gqa_pages_compact needs gqa_pages_workspace_size() bytes,

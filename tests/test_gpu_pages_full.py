@@ -1,6 +1,6 @@
-"""A pool that runs out while sequences that share a partly filled page are given pages of their own:
-what the first call has handed out is copied, pages are freed, the second call serves the rest, and
-every sequence's rows are what it appended."""
+"""Page calls at the ends: a pool that runs out while sequences that share a partly filled page are
+given pages of their own (what the first call has handed out is copied, pages are freed, the second
+call serves the rest, and every sequence's rows are what it appended), and lists of nothing."""
 import pytest
 import torch
 
@@ -58,3 +58,14 @@ def test_rows_survive_a_full_pool(dtype, layers):
             for kv, pool in enumerate((k, v)):
                 have = pool[table[b, 0].long(), :filled + 1].cpu()
                 assert torch.equal(have, torch.cat([rows[b][layer][kv], new[layer][kv][b:b + 1]]))
+
+
+def test_empty_lists():
+    """A step in which nothing has ended and nothing moves."""
+    table, lens, refs = i32([[0, -1], [1, -1]]), i32([5, 3]), i32([1, 1, 0, 0])
+    pool = torch.ones((4, 8, 2, 64), dtype=torch.bfloat16, device="cuda")
+    gqa.pages_free(i32([]), table, lens, refs)
+    gqa.pages_copy(pool, pool.clone(), torch.empty((0, 2), dtype=torch.int32, device="cuda"))
+    assert refs.tolist() == [1, 1, 0, 0] and lens.tolist() == [5, 3] and table.tolist() == [[0, -1], [1, -1]]
+    with pytest.raises(ValueError):  # checked all the same
+        gqa.pages_free(i32([]), table, lens, refs.long())
