@@ -15,8 +15,18 @@ TYPES = pytest.mark.parametrize("dtype", list(NAMES), ids=NAMES.values())
 
 
 def launched(fn, *kernels):
-    result, names = kernels_of(fn)
-    assert names is None or names == set(kernels)
+    """fn(), which launches these span kernels and no others.  The profiler drops a record now and then, so
+    what is missing is looked for again; what is too much counts at once."""
+    seen, recorded = set(), False
+    for _ in range(5):
+        result, names = kernels_of(fn)
+        if names is not None:
+            recorded = True
+            seen |= names
+            assert seen <= set(kernels)
+            if seen == set(kernels):
+                return result
+    assert not recorded, (seen, kernels)
     return result
 
 
